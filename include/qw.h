@@ -36,7 +36,7 @@
  *   - The return value is a qw_status.  qw_last_error_string() describes the
  *     last failure on the calling thread.
  *   - A size of zero tokens is a valid no-op and returns QW_OK.
- *   - Workspaces (qw_attention_decode, qw_lm_head; sizes from the
+ *   - Workspaces (the attention entry points, qw_lm_head; sizes from the
  *     *_workspace_size queries) begin with 64 KiB of completion counters
  *     followed by scratch.  Zero-fill a workspace once when it is allocated;
  *     every call leaves the counters at zero again, so one workspace serves
@@ -76,7 +76,12 @@ typedef enum {
   QW_ERR_WORKSPACE = 6    /* workspace pointer missing or too small */
 } qw_status;
 
-typedef enum { QW_BF16 = 0, QW_F32 = 1 } qw_dtype;
+typedef enum {
+  QW_BF16 = 0,
+  QW_F32 = 1,
+  QW_I8 = 2,   /* the codes of an 8-bit KV cache (kv_dtype arguments only) */
+  QW_E4M3 = 3
+} qw_dtype;
 
 typedef enum {
   QW_GEMM_COLUMN = 0,     /* W cut along the output dim ([TP] §3, tp_dim = 0) */
@@ -99,10 +104,11 @@ const char* qw_last_error_string(void);
  * Bounded waits inside the tensor-core and decode kernels set them when they
  * give up (a wait that should never time out; it exists so that a broken
  * pipeline returns instead of hanging the GPU): QW_ERR_TIMEOUT.  Decode
- * attention also records a context_lens entry larger than the max_context of
- * its call (the keys past max_context were not read, so that output is
- * wrong): QW_ERR_INVALID_ARG.  Returns QW_OK, QW_ERR_TIMEOUT or
- * QW_ERR_INVALID_ARG (QW_ERR_CUDA if the synchronisation fails).
+ * attention, and attention over the 8-bit cache, also record a context_lens
+ * entry larger than the max_context of their call (the keys past max_context
+ * were not read, so that output is wrong): QW_ERR_INVALID_ARG.  Returns QW_OK,
+ * QW_ERR_TIMEOUT or QW_ERR_INVALID_ARG (QW_ERR_CUDA if the synchronisation
+ * fails).
  */
 int qw_device_error(void* stream);
 
@@ -290,6 +296,101 @@ int qw_attention_prefill_paged(const void* q, const void* k_cache, const void* v
                                const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, const int32_t* block_table,
                                int max_blocks, int block_size, int n_seqs, int max_seqlen_q, int n_heads,
                                int n_kv_heads, int head_dim, float scale, void* out, int dtype, void* stream);
+
+/*
+ * KV cache in 8 bits ([SK] §7: the paged cache of qw_attention_decode_paged at
+ * half the bytes).  The four entry points share these arguments:
+ *   k_cache, v_cache  one-byte codes [num_slots, nkv, 128], 16-byte aligned;
+ *       kv_dtype QW_I8 (codes -127 .. 127) or QW_E4M3 (the e4m3 patterns that
+ *       stand for NaN are never written and read as +-480)
+ *   k_scale, v_scale  float [num_slots / scale_block, nkv]: the scale of each
+ *       aligned block of scale_block rows (16, 32 or 64; num_slots a multiple
+ *       of it) and kv head.  An element's value is code * scale; a scale below
+ *       2^-100 counts as 0.
+ *   block_table int32 [n_seqs, max_blocks], block_size (a multiple of 64): as
+ *       for the paged entry points.  Keys whose page is negative, beyond the
+ *       table or outside [0, num_slots) read as zeros and are not written.
+ *   context_lens int32 [n_seqs]: keys of each sequence, this call's new tokens
+ *       included; cu_seqlens_q int32 [n_seqs + 1]: sequence s has the new
+ *       tokens cu_seqlens_q[s] .. cu_seqlens_q[s+1] - 1, and new token i of Lq
+ *       sits at key position context_lens[s] - Lq + i.
+ * All are bf16 with head_dim 128.  Errors: QW_ERR_DTYPE (dtype, kv_dtype),
+ * QW_ERR_SHAPE (head_dim, heads, scale_block, block_size, num_slots,
+ * max_context), QW_ERR_INVALID_ARG (null or misaligned pointers, negative
+ * sizes), QW_ERR_WORKSPACE.
+ *
+ * qw_kv8_append: qw_qkv_norm_rope_store_kv into this cache: per-head
+ * QK-RMSNorm, RoPE, q out, k and v quantised.
+ *   qkv, n_heads, n_kv_heads, tp, positions, cos_sin, max_position, q_gamma,
+ *   k_gamma, eps, q_out: as for qw_qkv_norm_rope_store_kv, q_out bit for bit.
+ *   cu_seqlens_q NULL: one token per sequence (decode), T >= n_seqs.
+ *   Rows of qkv that belong to no sequence are padding: their q_out rows are
+ *   left as they were.
+ * k is normed and roped in fp32 and rounded once, by the quantiser.  For each
+ * scale block and kv head that gets new tokens, with C = 127 or 448:
+ *   scale = max(old, top / C), top the largest finite |value| of the new
+ *   tokens in the block (top / C below 2^-100 counts as 0); old is the block's
+ *   scale if it holds tokens before the first new one, else 0.
+ *   new codes = round(value * (1 / scale)) to nearest even, clamped to +-C;
+ *   NaN becomes 0.  Where the scale grew, the codes of the block's earlier
+ *   tokens become round(code * (old * (1 / scale))).
+ * Each growth adds at most half a step of the new scale to an earlier token's
+ * error.  A new token at a negative key position (a padding sequence with
+ * context_lens 0) is not stored.  Two sequences must not append to the same
+ * scale block in one call.  err_count: +1 per token whose position is outside
+ * the RoPE table (its q is zero, its k and v are stored as zeros) or whose
+ * page is missing.  Rules: tp divides nh and nkv.
+ */
+int qw_kv8_append(const void* qkv, int64_t T, int n_heads, int n_kv_heads, int head_dim, int tp,
+                  const int64_t* positions, const float* cos_sin, int64_t max_position, const void* q_gamma,
+                  const void* k_gamma, float eps, const int32_t* cu_seqlens_q, const int32_t* context_lens,
+                  const int32_t* block_table, int max_blocks, int block_size, int n_seqs, void* k_cache, void* v_cache,
+                  float* k_scale, float* v_scale, int64_t num_slots, int scale_block, void* q_out, int32_t* err_count,
+                  int dtype, int kv_dtype, void* stream);
+
+/*
+ * Values of chosen rows of the 8-bit cache, for instance to move a prefix into
+ * a bf16 cache: rows int64 [n_rows] (the same row may occur again), k_out and
+ * v_out dtype [n_rows, nkv, 128] (either may be NULL), each code * scale
+ * rounded once.  Row -1 gives zeros; so does a row outside [0, num_slots),
+ * which also counts in err_count.  dtype QW_BF16 or QW_F32.
+ */
+int qw_kv8_read(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                int64_t num_slots, int scale_block, int n_kv_heads, int head_dim, const int64_t* rows, int64_t n_rows,
+                void* k_out, void* v_out, int32_t* err_count, int dtype, int kv_dtype, void* stream);
+
+/*
+ * Attention over the 8-bit cache, with a sliding window and first tokens that
+ * stay visible: the query at key position p sees the keys j <= p with
+ * j > p - window or j < n_sink; window 0 means every key j <= p.  A query that
+ * sees no key gets a zero row.  nh / nkv from 1 to 16, any whole number.
+ *   q, out bf16 [tokens, nh, 128], 16-byte aligned; scale: the softmax scale.
+ *   max_context >= every context_lens[s], at most max_blocks * block_size (it
+ *   sizes the split of the keys; a larger entry is recorded for
+ *   qw_device_error, and the keys from max_context on are not read).
+ *   workspace: *_workspace_size bytes, zero-filled when allocated; may be NULL
+ *   only when that size is 0.
+ * qw_attention_decode_kv8: one query per sequence, at its last key.
+ * qw_attention_prefill_kv8: causal attention of packed new tokens whose k and
+ *   v are in the cache already (qw_kv8_append first).  total_q: rows of q;
+ *   max_seqlen_q >= every Lq (queries behind it get no output).  Rows of q
+ *   that belong to no sequence are padding: their out rows are left as they
+ *   were.
+ */
+int qw_attention_decode_kv8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                            const float* v_scale, int64_t num_slots, int scale_block, const int32_t* context_lens,
+                            const int32_t* block_table, int max_blocks, int block_size, int B, int max_context,
+                            int n_heads, int n_kv_heads, int head_dim, float scale, int window, int n_sink, void* out,
+                            void* workspace, size_t workspace_bytes, int dtype, int kv_dtype, void* stream);
+size_t qw_attention_decode_kv8_workspace_size(int B, int max_context, int n_heads, int n_kv_heads);
+int qw_attention_prefill_kv8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                             const float* v_scale, int64_t num_slots, int scale_block, const int32_t* cu_seqlens_q,
+                             const int32_t* context_lens, const int32_t* block_table, int max_blocks, int block_size,
+                             int n_seqs, int64_t total_q, int max_seqlen_q, int max_context, int n_heads,
+                             int n_kv_heads, int head_dim, float scale, int window, int n_sink, void* out,
+                             void* workspace, size_t workspace_bytes, int dtype, int kv_dtype, void* stream);
+size_t qw_attention_prefill_kv8_workspace_size(int n_seqs, int64_t total_q, int max_seqlen_q, int max_context,
+                                               int n_heads, int n_kv_heads);
 
 /*
  * Decode step's QK-RMSNorm + RoPE + KV-cache store ([SK] §3, §7.1, §8) and

@@ -18,7 +18,7 @@ _LIB_PATH = Path(__file__).resolve().parent / "libqw.so"
 _lib = None
 
 QW_OK, QW_ERR_INVALID_ARG, QW_ERR_SHAPE, QW_ERR_DTYPE, QW_ERR_CUDA, QW_ERR_TIMEOUT, QW_ERR_WORKSPACE = range(7)
-QW_BF16, QW_F32 = 0, 1
+QW_BF16, QW_F32, QW_I8, QW_E4M3 = range(4)
 QW_GEMM_COLUMN, QW_GEMM_ROW_REDUCE = 0, 1
 QW_EPI_NONE, QW_EPI_SILU_MUL = 0, 1
 
@@ -45,6 +45,15 @@ SIGNATURES = {
                                             _p, _p, _sz, _i32, _i32, _p]),
     "qw_attention_prefill_paged": (C.c_int, [_p, _p, _p, _i64, _p, _p, _p, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
                                              _f32, _p, _i32, _p]),
+    "qw_kv8_append": (C.c_int, [_p, _i64, _i32, _i32, _i32, _i32, _p, _p, _i64, _p, _p, _f32, _p, _p, _p, _i32, _i32, _i32,
+                                _p, _p, _p, _p, _i64, _i32, _p, _p, _i32, _i32, _p]),
+    "qw_kv8_read": (C.c_int, [_p, _p, _p, _p, _i64, _i32, _i32, _i32, _p, _i64, _p, _p, _p, _i32, _i32, _p]),
+    "qw_attention_decode_kv8": (C.c_int, [_p, _p, _p, _p, _p, _i64, _i32, _p, _p, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                          _f32, _i32, _i32, _p, _p, _sz, _i32, _i32, _p]),
+    "qw_attention_decode_kv8_workspace_size": (C.c_size_t, [_i32, _i32, _i32, _i32]),
+    "qw_attention_prefill_kv8": (C.c_int, [_p, _p, _p, _p, _p, _i64, _i32, _p, _p, _p, _i32, _i32, _i32, _i64, _i32, _i32,
+                                           _i32, _i32, _i32, _f32, _i32, _i32, _p, _p, _sz, _i32, _i32, _p]),
+    "qw_attention_prefill_kv8_workspace_size": (C.c_size_t, [_i32, _i64, _i32, _i32, _i32, _i32]),
     "qw_attention_decode_rope": (C.c_int, [_p, _i32, _i32, _i32, _i32, _p, _p, _i64, _p, _p, _f32, _p, _p, _p, _i64,
                                            _p, _p, _p, _i32, _i32, _f32, _p, _p, _sz, _i32, _i32, _p]),
     "qw_attention_decode_static": (C.c_int, [_p, _p, _p, _i64, _p, _p, _i32, _i32, _i32, _i32, _i32, _f32, _p, _i32,
@@ -266,6 +275,84 @@ def attention_prefill_paged(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, blo
         _dev_ptr(cu_seqlens_q, "cu_seqlens_q"), _dev_ptr(cu_seqlens_k, "cu_seqlens_k"),
         _dev_ptr(block_table, "block_table"), block_table.shape[1], block_size, n_seqs, max_seqlen_q, n_heads,
         n_kv_heads, head_dim, scale, _dev_ptr(out, "out"), dtype_code(q.dtype), _stream(stream)))
+
+
+def kv_code(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+            scale_block: int) -> int:
+    """kv_dtype of an 8-bit cache; the library sees pointers only, so the tensors' types and sizes are checked here."""
+    if k_cache.dtype not in (torch.int8, torch.float8_e4m3fn) or v_cache.dtype != k_cache.dtype:
+        raise QwError(QW_ERR_DTYPE, f"caches must both be int8 or float8_e4m3fn, not {k_cache.dtype} and {v_cache.dtype}")
+    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+        raise QwError(QW_ERR_DTYPE, "scales must be float32")
+    slots, nkv = k_cache.shape[0], k_cache.shape[1]
+    if v_cache.shape != k_cache.shape or scale_block <= 0 or any(
+            tuple(t.shape) != (slots // scale_block, nkv) for t in (k_scale, v_scale)):
+        raise QwError(QW_ERR_SHAPE, f"caches {tuple(k_cache.shape)} and {tuple(v_cache.shape)} need scales of "
+                                    f"[{slots} / {scale_block}, {nkv}]")
+    return QW_I8 if k_cache.dtype == torch.int8 else QW_E4M3
+
+
+def kv8_append(qkv, n_heads, n_kv_heads, head_dim, tp, positions, cos_sin, q_gamma, k_gamma, eps, cu_seqlens_q,
+               context_lens, block_table, block_size, k_cache, v_cache, k_scale, v_scale, scale_block, q_out,
+               err_count=None, stream=None):
+    """QK-norm + RoPE, q out, k and v quantised into an 8-bit paged cache; cu_seqlens_q None: one token per sequence."""
+    kv = kv_code(k_cache, v_cache, k_scale, v_scale, scale_block)
+    _check(load().qw_kv8_append(
+        _dev_ptr(qkv, "qkv"), qkv.shape[0], n_heads, n_kv_heads, head_dim, tp, _dev_ptr(positions, "positions"),
+        _dev_ptr(cos_sin, "cos_sin"), cos_sin.shape[0], _dev_ptr(q_gamma, "q_gamma"), _dev_ptr(k_gamma, "k_gamma"), eps,
+        _dev_ptr(cu_seqlens_q, "cu_seqlens_q"), _dev_ptr(context_lens, "context_lens"),
+        _dev_ptr(block_table, "block_table"), block_table.shape[1], block_size, context_lens.shape[0],
+        _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), _dev_ptr(k_scale, "k_scale"),
+        _dev_ptr(v_scale, "v_scale"), k_cache.shape[0], scale_block, _dev_ptr(q_out, "q_out"),
+        _dev_ptr(err_count, "err_count"), dtype_code(qkv.dtype), kv, _stream(stream)))
+
+
+def kv8_read(k_cache, v_cache, k_scale, v_scale, scale_block, rows, k_out, v_out, err_count=None, stream=None):
+    """Values of the 8-bit cache's rows (int64 [n]); k_out or v_out may be None."""
+    kv = kv_code(k_cache, v_cache, k_scale, v_scale, scale_block)
+    out = k_out if k_out is not None else v_out
+    _check(load().qw_kv8_read(
+        _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), _dev_ptr(k_scale, "k_scale"),
+        _dev_ptr(v_scale, "v_scale"), k_cache.shape[0], scale_block, k_cache.shape[1], k_cache.shape[2],
+        _dev_ptr(rows, "rows"), rows.shape[0], _dev_ptr(k_out, "k_out"), _dev_ptr(v_out, "v_out"),
+        _dev_ptr(err_count, "err_count"), dtype_code(out.dtype) if out is not None else QW_BF16, kv, _stream(stream)))
+
+
+def attention_decode_kv8_workspace_size(B, max_context, n_heads, n_kv_heads) -> int:
+    return load().qw_attention_decode_kv8_workspace_size(B, max_context, n_heads, n_kv_heads)
+
+
+def attention_decode_kv8(q, k_cache, v_cache, k_scale, v_scale, scale_block, context_lens, block_table, block_size,
+                         max_context, n_heads, n_kv_heads, head_dim, scale, out, workspace, window=0, n_sink=0,
+                         stream=None):
+    """Decode attention over an 8-bit paged cache; window > 0: the last `window` keys and the first n_sink are seen."""
+    kv = kv_code(k_cache, v_cache, k_scale, v_scale, scale_block)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(load().qw_attention_decode_kv8(
+        _dev_ptr(q, "q"), _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), _dev_ptr(k_scale, "k_scale"),
+        _dev_ptr(v_scale, "v_scale"), k_cache.shape[0], scale_block, _dev_ptr(context_lens, "context_lens"),
+        _dev_ptr(block_table, "block_table"), block_table.shape[1], block_size, q.shape[0], max_context, n_heads,
+        n_kv_heads, head_dim, scale, window, n_sink, _dev_ptr(out, "out"), _dev_ptr(workspace, "workspace"), ws_bytes,
+        dtype_code(q.dtype), kv, _stream(stream)))
+
+
+def attention_prefill_kv8_workspace_size(n_seqs, total_q, max_seqlen_q, max_context, n_heads, n_kv_heads) -> int:
+    return load().qw_attention_prefill_kv8_workspace_size(n_seqs, total_q, max_seqlen_q, max_context, n_heads, n_kv_heads)
+
+
+def attention_prefill_kv8(q, k_cache, v_cache, k_scale, v_scale, scale_block, cu_seqlens_q, context_lens, block_table,
+                          block_size, max_seqlen_q, max_context, n_heads, n_kv_heads, head_dim, scale, out, workspace,
+                          window=0, n_sink=0, stream=None):
+    """Causal attention of packed new tokens over an 8-bit paged cache that holds their k and v already."""
+    kv = kv_code(k_cache, v_cache, k_scale, v_scale, scale_block)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(load().qw_attention_prefill_kv8(
+        _dev_ptr(q, "q"), _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), _dev_ptr(k_scale, "k_scale"),
+        _dev_ptr(v_scale, "v_scale"), k_cache.shape[0], scale_block, _dev_ptr(cu_seqlens_q, "cu_seqlens_q"),
+        _dev_ptr(context_lens, "context_lens"), _dev_ptr(block_table, "block_table"), block_table.shape[1], block_size,
+        context_lens.shape[0], q.shape[0], max_seqlen_q, max_context, n_heads, n_kv_heads, head_dim, scale, window,
+        n_sink, _dev_ptr(out, "out"), _dev_ptr(workspace, "workspace"), ws_bytes, dtype_code(q.dtype), kv,
+        _stream(stream)))
 
 
 def attention_decode_static(q, k_cache, v_cache, context_lens, seq_base, max_context, n_heads, n_kv_heads,

@@ -1,0 +1,118 @@
+// The 8-bit paged KV cache: codes, block scales and page lookup shared by the
+// kernels that write it (kv8_cache.cu) and read it (attention_kv8*.cu).
+//
+// A cache row (one token) holds n_kv_heads x 128 one-byte codes; every aligned
+// block of `scale_block` rows has one fp32 scale for each kv head, and an
+// element's value is code * scale.  Codes are int8 in [-127, 127] or e4m3; the
+// two e4m3 bit patterns that stand for NaN are never written, and are read as
+// +-480, so that whatever a recycled page holds is finite.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace qw {
+namespace kv8 {
+
+constexpr int HD = 128;
+// A block scale below this is stored as zero with zero codes: 1 / scale stays
+// finite, and the attention kernels' logarithm of a scale stays in range.
+constexpr float kTinyScale = 7.888609052210118e-31f;   // 2^-100
+
+// KV: QW_I8 or QW_E4M3
+template <int KV> __device__ constexpr float code_max() { return KV == QW_I8 ? 127.0f : 448.0f; }
+
+// The e4m3 bits placed in an f16 give the value times 2^-8 (the exponent biases
+// are 7 and 15); exact for every code, subnormals included.
+__device__ __forceinline__ float code_f32_e4m3(uint32_t b) {
+  const uint32_t h = ((b & 0x80u) << 8) | ((b & 0x7fu) << 7);
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(h))) * 256.0f;
+}
+template <int KV> __device__ __forceinline__ float code_f32(uint32_t b) {
+  if constexpr (KV == QW_I8) return float(int(b << 24) >> 24);
+  else return code_f32_e4m3(b);
+}
+// four codes of a word
+template <int KV> __device__ __forceinline__ void codes_f32(uint32_t w, float* f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = code_f32<KV>((w >> (8 * i)) & 0xffu);
+}
+
+// Four values already divided by their scale -> codes: round to nearest even,
+// clamped to the largest code; NaN becomes 0.
+template <int KV> __device__ __forceinline__ uint32_t quant4(const float* x) {
+  if constexpr (KV == QW_I8) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w |= (uint32_t(min(max(__float2int_rn(x[i]), -127), 127)) & 0xffu) << (8 * i);
+    return w;
+  } else {
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = x[i] == x[i] ? x[i] : 0.0f;
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+  }
+}
+
+// The cache as the entry points get it.
+struct Cache {
+  const void* k;
+  const void* v;
+  const float* k_scale;   // [num_slots / scale_block, nkv]
+  const float* v_scale;
+  int64_t num_slots;
+  int sb_shift;           // log2(scale_block)
+  const int32_t* table;   // [n_seqs, max_blocks]
+  int max_blocks;
+  int block_size;
+};
+
+// Cache row of key position p of sequence s, or -1 where the block table has no
+// such page or the page lies outside the cache.
+__device__ __forceinline__ int64_t row_of(const int32_t* table, int max_blocks, int block_size, int64_t num_slots,
+                                          int s, int p) {
+  const int blk = p / block_size;
+  if (blk >= max_blocks) return -1;
+  const int page = table[int64_t(s) * max_blocks + blk];
+  const int64_t row = int64_t(page) * block_size + (p - blk * block_size);
+  return page >= 0 && row < num_slots ? row : -1;
+}
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline int scale_shift(int scale_block) {
+  return scale_block == 16 ? 4 : scale_block == 32 ? 5 : scale_block == 64 ? 6 : -1;
+}
+
+// Checks shared by the entry points on the cache; QW_OK or the error set.
+inline int check_cache(const char* who, const void* k, const void* v, const float* ks, const float* vs,
+                       int64_t num_slots, int scale_block, int kv_dtype) {
+  if (kv_dtype != QW_I8 && kv_dtype != QW_E4M3)
+    return set_error(QW_ERR_DTYPE, "%s: kv_dtype %d is neither QW_I8 nor QW_E4M3", who, kv_dtype);
+  if (scale_shift(scale_block) < 0)
+    return set_error(QW_ERR_SHAPE, "%s: scale_block %d must be 16, 32 or 64", who, scale_block);
+  if (num_slots < 0 || num_slots > INT32_MAX)
+    return set_error(QW_ERR_INVALID_ARG, "%s: num_slots %lld", who, (long long)num_slots);
+  if (num_slots % scale_block)
+    return set_error(QW_ERR_SHAPE, "%s: num_slots %lld is not a multiple of scale_block %d", who, (long long)num_slots,
+                     scale_block);
+  if (!k || !v || !ks || !vs) return set_error(QW_ERR_INVALID_ARG, "%s: null cache or scale pointer", who);
+  if (!aligned16(k) || !aligned16(v)) return set_error(QW_ERR_INVALID_ARG, "%s: caches must be 16-byte aligned", who);
+  if ((reinterpret_cast<uintptr_t>(ks) | reinterpret_cast<uintptr_t>(vs)) & 3u)
+    return set_error(QW_ERR_INVALID_ARG, "%s: scales must be 4-byte aligned", who);
+  return QW_OK;
+}
+inline int check_table(const char* who, const int32_t* table, int max_blocks, int block_size, int scale_block) {
+  if (!table) return set_error(QW_ERR_INVALID_ARG, "%s: null block table", who);
+  if (max_blocks <= 0 || block_size <= 0 || block_size % 64)
+    return set_error(QW_ERR_SHAPE, "%s: block_size %d must be a positive multiple of 64, max_blocks positive", who,
+                     block_size);
+  (void)scale_block;   // 16, 32 or 64: divides block_size
+  return QW_OK;
+}
+
+}  // namespace kv8
+}  // namespace qw

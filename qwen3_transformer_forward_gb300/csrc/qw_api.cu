@@ -40,6 +40,7 @@ unsigned int take_tc_timeouts();
 unsigned int take_attn_timeouts();
 unsigned int take_prefill_timeouts();
 unsigned int take_dstep_errors();
+unsigned int take_kv8_errors();
 
 }  // namespace qw
 
@@ -51,16 +52,17 @@ extern "C" int qw_device_error(void* stream) {
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return qw::set_error(QW_ERR_CUDA, "qw_device_error: %s", cudaGetErrorString(e));
   const unsigned int gemm = qw::take_tc_timeouts(), dec_word = qw::take_attn_timeouts(),
-                     pre = qw::take_prefill_timeouts(), step = qw::take_dstep_errors();
-  const unsigned int dec = dec_word & ~qw::kErrContextOverflow;
-  if (gemm | dec | pre | step)
+                     pre = qw::take_prefill_timeouts(), step = qw::take_dstep_errors(),
+                     kv8_word = qw::take_kv8_errors();
+  const unsigned int dec = dec_word & ~qw::kErrContextOverflow, kv8 = kv8_word & ~qw::kErrContextOverflow;
+  if (gemm | dec | pre | step | kv8)
     return qw::set_error(QW_ERR_TIMEOUT,
                          "a bounded device-side wait timed out (gemm 0x%x, decode attention 0x%x, prefill attention "
-                         "0x%x, decode step 0x%x)",
-                         gemm, dec, pre, step);
-  if (dec_word & qw::kErrContextOverflow)
+                         "0x%x, decode step 0x%x, 8-bit cache attention 0x%x)",
+                         gemm, dec, pre, step, kv8);
+  if ((dec_word | kv8_word) & qw::kErrContextOverflow)
     return qw::set_error(QW_ERR_INVALID_ARG,
-                         "decode attention: a context_lens entry exceeded the call's max_context; the keys past it "
+                         "attention: a context_lens entry exceeded the call's max_context; the keys past it "
                          "were not read");
   return QW_OK;
 }
