@@ -2,7 +2,10 @@
 // window and first tokens that stay visible.
 #include <math.h>
 
+#include <algorithm>
+
 #include "kv8.cuh"
+#include "tc_common.cuh"
 
 namespace qw {
 namespace kv8 {
@@ -77,6 +80,585 @@ int launch_attn(const void* q, const Cache& c, const int32_t* cu_q, const int32_
   return check_launch("attn_kv8_kernel");
 }
 
+// ---------------------------------------------------------------------------
+// decode
+//
+// A tile is KT = 128 / HG tokens of HG kv heads (HG = 8, 4, 2 or 1, the group of
+// kv heads that a CTA reads together): 16 KB of K and 16 KB of V, which sit side
+// by side in memory, so that the copies of one tile cover whole DRAM rows however
+// the tiles are dealt out.  One CTA per SM.  Every CTA sums the sequences' visible
+// tiles (their lengths are on the device) and takes an equal, contiguous share:
+// ragged batches and windows stay balanced.  A producer warp streams the share
+// through a ring of stages (TMA boxes of 16 tokens x HG heads, which lie in one
+// page and one scale block; 128-byte swizzle; the block scales by 4-byte
+// asynchronous copies on the same barrier).  Eight consumer warps each take the
+// 16 keys x 128 dims of one kv head:
+//   S^T [16 keys, 8 heads] = K Q^T   8 mma.m16n8k16: keys are the rows, so that a
+//   O^T [128 dims, 8 heads] += V^T P  group of up to 8 q heads fills the columns
+// Operands are f16: codes are exact in it, q is moved by a power of two per row
+// (exact, see row_scale), weights keep 11 bits.  The order of the dims inside a
+// k-step is free as long as Q and K share it, so a lane loads 16 codes at a time
+// and converts them in registers, without ldmatrix.  A step's 16 keys share one
+// scale: with x = score * log2 e * k_scale + log2(v_scale), the running maximum m
+// is over x, the weights are 2^(x - m + 15) <= 2^15 (f16 keeps 11 bits down to
+// 2^-29 of the largest), O takes the codes of V alone, and the denominator is
+// sum 2^(x - m) / v_scale, in fp32.
+// A (sequence, kv head) that ends inside one CTA is written out; otherwise every
+// CTA of it leaves (m, l, O) in the workspace slot (CTA + pair), distinct for each
+// that occurs, and the last to finish, by the pair's counter, adds them in CTA
+// order.
+// ---------------------------------------------------------------------------
+constexpr int DK_WARPS = 8, DK_THREADS = 32 * (DK_WARPS + 1);
+constexpr int DK_CTAS = 152;                       // at most one CTA per SM
+constexpr uint32_t DK_SUB = 2048;                  // 16 keys x 128 codes of one kv head
+constexpr uint32_t DK_STAGE = 2 * DK_WARPS * DK_SUB;
+constexpr int DK_MIN_TILES = 8;                    // tiles that a CTA gets at least
+constexpr float kShift = 15.0f;                    // weights are held times 2^15
+constexpr float kUnshift = 1.0f / 32768.0f;
+
+template <int HG, int NT> __host__ __device__ constexpr int dk_stages() { return HG == DK_WARPS ? 6 : NT == 1 ? 5 : 4; }
+// ring | merge [8 warps][36 NT words][32 lanes], with several warps per kv head | scales | barriers
+template <int HG, int NT> __host__ __device__ constexpr uint32_t dk_merge_bytes() {
+  return HG == DK_WARPS ? 0u : uint32_t(DK_WARPS) * 36u * NT * 128u;
+}
+template <int HG, int NT> __host__ __device__ constexpr size_t dk_smem() {
+  static_assert(1024 + dk_stages<HG, NT>() * (DK_STAGE + 2 * DK_WARPS * 4 + 16) + dk_merge_bytes<HG, NT>() + 512 <= 232448,
+                "shared memory of one CTA");
+  return 1024 + size_t(dk_stages<HG, NT>()) * (DK_STAGE + 2 * DK_WARPS * 4 + 16) + dk_merge_bytes<HG, NT>() + 256;
+}
+
+struct DecodeArgs {
+  const bf16* q;
+  const int32_t* ctx;
+  Cache c;
+  int B, nh, nkv, G, nhg;   // G: q heads of a kv head; nhg: groups of HG kv heads
+  int max_ctx, window, n_sink;
+  float scale_log2;
+  float* ws_o;              // [slots][HG][G][128]
+  float* ws_ml;             // [slots][HG][G][2]
+  unsigned int* counters;   // [B * nkv]
+  bf16* out;
+};
+
+__device__ __forceinline__ Span decode_span(int ctx, int max_ctx, int window, int n_sink, int kt) {
+  Span s;
+  s.L = max(min(ctx, max_ctx), 0);
+  s.lo = window > 0 ? max(ctx - window, 0) : 0;
+  const int tb = (s.L + kt - 1) / kt;
+  s.w0 = s.lo / kt;
+  s.ns = min(min((min(n_sink, s.lo) + kt - 1) / kt, s.w0), tb);
+  s.nt = s.ns + max(tb - s.w0, 0);
+  return s;
+}
+__device__ __forceinline__ bool any_visible(const Span& s, int n_sink, int key0) {   // of 16 keys from key0
+  return max(key0, s.lo) < min(key0 + 16, s.L) || key0 < min(n_sink, s.L);
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ unsigned int atom_add_acq_rel(unsigned int* p, unsigned int v) {
+  unsigned int old;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
+}
+__device__ __forceinline__ void cp_async4_zfill(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {   // when this thread's copies so far have landed
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Writes 16 outputs of one head: dims 16 gq .. + 15.
+__device__ __forceinline__ void store_out16(bf16* o, const float (&f)[16]) {
+  store16(o, f);
+  store16(o + 8, f + 8);
+}
+
+template <int KV, int HG, int NT>
+__global__ void __launch_bounds__(DK_THREADS, 1) attn_decode_kv8_kernel(const __grid_constant__ CUtensorMap tmK,
+                                                                       const __grid_constant__ CUtensorMap tmV,
+                                                                       const DecodeArgs a) {
+  constexpr int KS = DK_WARPS / HG, KT = 16 * KS, ST = dk_stages<HG, NT>();
+  constexpr uint32_t kBox = 16 * HG * HD;            // bytes of one TMA box
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+  const uint32_t ring = smem_u32(sm);
+  float* merge = reinterpret_cast<float*>(sm + ST * DK_STAGE);
+  float* scales = reinterpret_cast<float*>(sm + ST * DK_STAGE + dk_merge_bytes<HG, NT>());   // [ST][K, V][8]
+  const uint32_t bars = smem_u32(scales + ST * 2 * DK_WARPS);
+  auto full = [&](int s) { return bars + 8u * uint32_t(s); };
+  auto empty = [&](int s) { return bars + 8u * uint32_t(ST + s); };
+  __shared__ int64_t s_sum[DK_WARPS + 1];
+  __shared__ int64_t s_before;
+  __shared__ int s_first;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < ST; ++s) {
+      tcx::mbar_init(full(s), 33);
+      tcx::mbar_init(empty(s), DK_WARPS);
+    }
+    tcx::fence_mbar_init();
+    tcx::prefetch_map(&tmK);
+    tcx::prefetch_map(&tmV);
+  }
+  pdl_wait();      // inputs of this kernel are complete and visible
+  pdl_trigger();   // only now may the next kernel start its prologue
+
+  // ---- this CTA's share: an equal part of all sequences' visible tiles
+  auto span_of = [&](int b) { return decode_span(a.ctx[b], a.max_ctx, a.window, a.n_sink, KT); };
+  int64_t mine = 0;
+  for (int b = tid; b < a.B; b += DK_THREADS) mine += int64_t(span_of(b).nt) * a.nhg;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) s_sum[warp] = mine;
+  // sequences that see nothing: zero rows (dealt out over the warps of the grid)
+  for (int b = blockIdx.x + gridDim.x * warp; b < a.B; b += gridDim.x * (DK_WARPS + 1)) {
+    const int ctx = a.ctx[b];
+    if (ctx > a.max_ctx && lane == 0) atomicOr(&g_kv8_error, kErrContextOverflow);
+    if (span_of(b).nt == 0)
+      for (int i = lane; i < a.nh * HD / 8; i += 32)
+        *reinterpret_cast<uint4*>(a.out + int64_t(b) * a.nh * HD + 8 * i) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w <= DK_WARPS; ++w) total += s_sum[w];
+  const int64_t per = max(int64_t(DK_MIN_TILES), (total + gridDim.x - 1) / gridDim.x);
+  const int64_t lo = int64_t(blockIdx.x) * per, hi = min(total, lo + per);
+  if (lo >= hi) return;   // uniform over the CTA; no barrier is in use yet
+  if (warp == 0) {        // the sequence that holds tile `lo`: a scan, 32 sequences at a time
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const int b = b0 + lane;
+      const int64_t n = b < a.B ? int64_t(span_of(b).nt) * a.nhg : 0;
+      int64_t upto = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const bool here = lo >= before + upto - n && lo < before + upto;
+      if (here) {
+        s_first = b;
+        s_before = before + upto - n;
+      }
+      if (__any_sync(0xffffffffu, here)) break;
+      before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+  }
+  __syncthreads();
+  // position in the share: tile t of kv head group hg of sequence b; `start` is the
+  // first tile of that (sequence, group) in the common order
+  int b = s_first, hg, t;
+  Span sp = span_of(b);
+  {
+    const int64_t off = lo - s_before;
+    hg = int(off / sp.nt);
+    t = int(off % sp.nt);
+  }
+  const int count = int(hi - lo);
+  auto next_pair = [&]() {   // only while a tile is left
+    t = 0;
+    if (++hg == a.nhg) {
+      hg = 0;
+      do sp = span_of(++b);
+      while (sp.nt == 0);
+    }
+  };
+  bool ok = true;
+  auto wait = [&](uint32_t bar, uint32_t parity, unsigned int code) {
+    if (ok && !tcx::mbar_wait(bar, parity, &g_kv8_error, code)) ok = false;
+  };
+
+  if (warp == DK_WARPS) {
+    // ---------------- producer warp
+    int j = 0;
+    for (; j < count; ++j, ++t) {
+      if (t == sp.nt) next_pair();
+      const int s = j % ST;
+      if (j >= ST) wait(empty(s), uint32_t(j / ST - 1) & 1u, 0x1u);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      // the consumers read this stage through the generic proxy, the copies write through the async proxy
+      tcx::fence_proxy_async();
+      const int key0 = (sp.tile(t) * KS + (lane & (KS - 1))) * 16;   // lane ks < KS: 16 tokens of every head
+      const bool act = any_visible(sp, a.n_sink, key0);
+      const int64_t row = act ? row_of(a.c.table, a.c.max_blocks, a.c.block_size, a.c.num_slots, b, key0) : -1;
+      const unsigned boxes = __popc(__ballot_sync(0xffffffffu, act && lane < KS));
+      if (lane == 0) tcx::mbar_expect_tx(full(s), boxes * 2 * kBox);
+      __syncwarp();
+      if (act && lane < KS) {
+        const int y = row >= 0 ? int(row) : int(a.c.num_slots);      // outside: zeros
+        const uint32_t dst = ring + uint32_t(s) * DK_STAGE + uint32_t(lane) * kBox;
+        tcx::tma_load_3d(dst, &tmK, full(s), 0, y, hg * HG);
+        tcx::tma_load_3d(dst + DK_STAGE / 2, &tmV, full(s), 0, y, hg * HG);
+      }
+      // scales of consumer warp `lane`: its 16 keys are lane / HG, its kv head lane % HG
+      const int64_t wrow = __shfl_sync(0xffffffffu, row, (lane & 7) / HG);
+      const int g = hg * HG + lane % HG;
+      if (lane < DK_WARPS) {
+        const bool has = wrow >= 0 && g < a.nkv;
+        const int64_t at = has ? (wrow >> a.c.sb_shift) * a.nkv + g : 0;
+        const uint32_t dst = smem_u32(scales + s * 2 * DK_WARPS + lane);
+        cp_async4_zfill(dst, a.c.k_scale + at, has);
+        cp_async4_zfill(dst + 4 * DK_WARPS, a.c.v_scale + at, has);
+      }
+      cp_async_arrive(full(s));
+    }
+    // the last copy of each stage has landed before this CTA may end
+    for (int i = max(0, j - ST); i < j; ++i)
+      tcx::mbar_wait(full(i % ST), uint32_t(i / ST) & 1u, &g_kv8_error, 0x4u);
+    return;
+  }
+
+  // ---------------- consumer warps
+  const int gq = lane >> 2, tq = lane & 3;
+  const int h = warp % HG, ks = warp / HG;
+  int64_t start = lo - t;
+  int j = 0;
+  while (j < count) {
+    if (t == sp.nt) {
+      start += sp.nt;
+      next_pair();
+    }
+    const int g = hg * HG + h;
+    const bool head_ok = g < a.nkv;
+    const int n_seg = min(sp.nt - t, count - j);
+    // q: head column 8 nt + gq, dims 32 tq .. + 31, moved into f16's range
+    uint32_t qb[NT][8][2];
+    float qa[NT][2];   // score factor of heads 8 nt + 2 tq, + 1
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int hd = 8 * n + gq;
+      const bool has = head_ok && hd < a.G;
+      const bf16* src = a.q + (int64_t(b) * a.nh + (has ? g * a.G + hd : 0)) * HD + 32 * tq;
+      float f[32], top = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) load16(src + 8 * e, f + 8 * e);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        f[e] = has ? f[e] : 0.0f;
+        top = fmaxf(top, fabsf(f[e]));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      float mul, inv;
+      row_scale(top, mul, inv);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        qb[n][e][0] = pack_f16(f[4 * e] * mul, f[4 * e + 1] * mul);
+        qb[n][e][1] = pack_f16(f[4 * e + 2] * mul, f[4 * e + 3] * mul);
+      }
+      inv *= a.scale_log2 * pair_factor<KV>();
+      qa[n][0] = __shfl_sync(0xffffffffu, inv, 8 * tq);
+      qa[n][1] = __shfl_sync(0xffffffffu, inv, 8 * tq + 4);
+    }
+    float o[NT][8][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.0f;
+    }
+    for (int i = 0; i < n_seg; ++i, ++j, ++t) {
+      const int s = j % ST;
+      wait(full(s), uint32_t(j / ST) & 1u, 0x2u);
+      const int key0 = (sp.tile(t) * KS + ks) * 16;
+      if (head_ok && any_visible(sp, a.n_sink, key0)) {
+        const uint32_t sK = ring + uint32_t(s) * DK_STAGE + uint32_t(warp) * DK_SUB, sV = sK + DK_STAGE / 2;
+        const float sk = scales[s * 2 * DK_WARPS + warp], sv = scales[s * 2 * DK_WARPS + DK_WARPS + warp];
+        float c[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.0f;
+        {
+          // keys gq and gq + 8, dims 32 tq .. + 31 (16-byte chunks 2 tq, 2 tq + 1)
+          uint32_t k0[8], k1[8];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t at = sK + uint32_t(gq) * 128u + (uint32_t((2 * tq + u) ^ gq) << 4);
+            const uint4 x = lds128(at), y = lds128(at + 1024u);
+            k0[4 * u] = x.x; k0[4 * u + 1] = x.y; k0[4 * u + 2] = x.z; k0[4 * u + 3] = x.w;
+            k1[4 * u] = y.x; k1[4 * u + 1] = y.y; k1[4 * u + 2] = y.z; k1[4 * u + 3] = y.w;
+          }
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            uint32_t a0, a1, a2, a3;
+            word_pairs<KV>(k0[kk], a0, a2);
+            word_pairs<KV>(k1[kk], a1, a3);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16(c[n], a0, a1, a2, a3, qb[n][kk][0], qb[n][kk][1]);
+          }
+        }
+        // V: keys 2 tq, 2 tq + 1 and the same + 8, dims 16 gq .. + 15
+        uint4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = 2 * tq + (u & 1) + 8 * (u >> 1);
+          v[u] = lds128(sV + uint32_t(r) * 128u + (uint32_t(gq ^ (r & 7)) << 4));
+        }
+        const bool v_none = sv < kTinyScale;
+        const float svc = v_none ? kTinyScale : sv;
+        const float lsv = lg2(svc), isv = __fdividef(kUnshift, svc);
+        const bool all = key0 + 16 <= sp.L && (key0 >= sp.lo || key0 + 16 <= a.n_sink);
+        bool vis[2] = {true, true};
+        if (!all) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int kp = key0 + gq + 8 * u;
+            vis[u] = kp < sp.L && (kp >= sp.lo || kp < a.n_sink);
+          }
+        }
+        uint32_t pb[NT][2];
+        bool grew = false;
+        float al[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float f = qa[n][e] * sk;
+            const float x0 = vis[0] ? fmaf(c[n][e], f, lsv) : -INFINITY, x1 = vis[1] ? fmaf(c[n][e + 2], f, lsv) : -INFINITY;
+            float mx = fmaxf(x0, x1);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float m_new = fmaxf(m[n][e], mx);
+            grew |= m_new > m[n][e];
+            al[n][e] = ex2(m[n][e] - m_new);   // (a visible key is in the tile: m_new is finite)
+            m[n][e] = m_new;
+            p[e] = ex2(x0 - m_new + kShift);
+            p[e + 2] = ex2(x1 - m_new + kShift);
+            l[n][e] = fmaf(l[n][e], al[n][e], (p[e] + p[e + 2]) * isv);
+          }
+          pb[n][0] = transpose8(v_none ? 0u : pack_f16(p[0], p[1]));   // keys 2 tq, + 1 of head gq
+          pb[n][1] = transpose8(v_none ? 0u : pack_f16(p[2], p[3]));   // keys 8 + 2 tq, + 1
+        }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+              o[n][d][0] *= al[n][0];
+              o[n][d][1] *= al[n][1];
+              o[n][d][2] *= al[n][0];
+              o[n][d][3] *= al[n][1];
+            }
+        }
+        // O^T rows: tile d holds dims 16 gq + 2 d (row gq) and 16 gq + 2 d + 1 (row gq + 8)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t* vw[4] = {&v[0].x + w, &v[1].x + w, &v[2].x + w, &v[3].x + w};
+          uint32_t lo4[4], hi4[4];
+          cross_pairs<KV>(*vw[0], *vw[1], lo4);
+          cross_pairs<KV>(*vw[2], *vw[3], hi4);
+#pragma unroll
+          for (int d = 0; d < 2; ++d)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma_f16(o[n][2 * w + d], lo4[2 * d], lo4[2 * d + 1], hi4[2 * d], hi4[2 * d + 1], pb[n][0], pb[n][1]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) tcx::mbar_arrive(empty(s));
+    }
+    // ---- end of this CTA's part of the pair: sums over the lanes of a head, then over the head's warps
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
+        l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
+        l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
+      }
+    if constexpr (KS > 1) {
+      float* mw = merge + warp * 36 * NT * 32 + lane;
+      if (ks > 0) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mw[((n * 8 + i) * 4 + e) * 32] = o[n][i][e];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            mw[(32 * NT + 4 * n + e) * 32] = m[n][e];
+            mw[(32 * NT + 4 * n + 2 + e) * 32] = l[n][e];
+          }
+        }
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * DK_WARPS) : "memory");
+      if (ks == 0) {
+#pragma unroll 1
+        for (int w = h + HG; w < DK_WARPS; w += HG) {
+          const float* ow = merge + w * 36 * NT * 32 + lane;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float mine_[2], theirs[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float mo = ow[(32 * NT + 4 * n + e) * 32], lo_ = ow[(32 * NT + 4 * n + 2 + e) * 32];
+              const float mx = fmaxf(m[n][e], mo), mu = mx == -INFINITY ? 0.0f : mx;
+              mine_[e] = ex2(m[n][e] - mu);
+              theirs[e] = ex2(mo - mu);
+              m[n][e] = mx;
+              l[n][e] = l[n][e] * mine_[e] + lo_ * theirs[e];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                o[n][i][e] = o[n][i][e] * mine_[e & 1] + ow[((n * 8 + i) * 4 + e) * 32] * theirs[e & 1];
+          }
+        }
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * DK_WARPS) : "memory");   // the area is free again
+    }
+    if (ks == 0 && head_ok) {
+      const int c_first = int(start / per), c_last = int((start + sp.nt - 1) / per);
+      const bool split = c_first != c_last;
+      const int pair = b * a.nhg + hg;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int hd = 8 * n + 2 * tq + e;
+          if (hd >= a.G) continue;
+          float f[16];
+          const float fac = split ? 1.0f : (l[n][e] > 0.0f ? kUnshift * pair_factor<KV>() / l[n][e] : 0.0f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            f[2 * i] = o[n][i][e] * fac;
+            f[2 * i + 1] = o[n][i][e + 2] * fac;
+          }
+          if (!split) {
+            store_out16(a.out + (int64_t(b) * a.nh + g * a.G + hd) * HD + 16 * gq, f);
+          } else {
+            const int64_t idx = ((int64_t(blockIdx.x) + pair) * HG + h) * a.G + hd;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) store16(a.ws_o + idx * HD + 16 * gq + 4 * i, f + 4 * i);
+            if (gq == 0) {
+              a.ws_ml[2 * idx] = m[n][e];
+              a.ws_ml[2 * idx + 1] = l[n][e];
+            }
+          }
+        }
+      if (split) {
+        __threadfence();
+        __syncwarp();
+        unsigned int before = 0;
+        if (lane == 0) before = atom_add_acq_rel(a.counters + b * a.nkv + g, 1u);
+        before = __shfl_sync(0xffffffffu, before, 0);
+        if (before == unsigned(c_last - c_first)) {
+          __threadfence();
+          for (int hd = 0; hd < a.G; ++hd) {
+            auto index = [&](int c) { return ((int64_t(c) + pair) * HG + h) * a.G + hd; };
+            float M = -INFINITY;
+            for (int c = c_first + lane; c <= c_last; c += 32) M = fmaxf(M, __ldcg(a.ws_ml + 2 * index(c)));
+            M = warp_max(M);
+            const float mu = M == -INFINITY ? 0.0f : M;
+            float lsum = 0.0f;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int c0 = c_first; c0 <= c_last; c0 += 8) {
+              float wgt[8], lc[8];
+              float4 x[8];
+#pragma unroll
+              for (int u = 0; u < 8; ++u) {   // one batch of loads in flight together
+                const int64_t idx = index(min(c0 + u, c_last));
+                const bool in = c0 + u <= c_last;
+                wgt[u] = in ? ex2(__ldcg(a.ws_ml + 2 * idx) - mu) : 0.0f;
+                lc[u] = __ldcg(a.ws_ml + 2 * idx + 1);
+                x[u] = __ldcg(reinterpret_cast<const float4*>(a.ws_o + idx * HD) + lane);
+              }
+#pragma unroll
+              for (int u = 0; u < 8; ++u) {
+                lsum = fmaf(lc[u], wgt[u], lsum);
+                acc.x = fmaf(x[u].x, wgt[u], acc.x);
+                acc.y = fmaf(x[u].y, wgt[u], acc.y);
+                acc.z = fmaf(x[u].z, wgt[u], acc.z);
+                acc.w = fmaf(x[u].w, wgt[u], acc.w);
+              }
+            }
+            const float fac = lsum > 0.0f ? kUnshift * pair_factor<KV>() / lsum : 0.0f;
+            *reinterpret_cast<uint2*>(a.out + (int64_t(b) * a.nh + g * a.G + hd) * HD + 4 * lane) =
+                make_uint2(pack_bf16(acc.x * fac, acc.y * fac), pack_bf16(acc.z * fac, acc.w * fac));
+          }
+          if (lane == 0) a.counters[b * a.nkv + g] = 0u;
+        }
+      }
+    }
+  }
+}
+
+int head_group(int nkv) { return nkv > 4 ? 8 : nkv > 2 ? 4 : nkv; }
+
+// Room for the partial results: one (m, l, O) per (CTA, pair) that can occur.
+size_t decode_slots(int B, int nkv) {
+  const int hg = head_group(nkv);
+  return size_t(DK_CTAS) + size_t(B) * ((nkv + hg - 1) / hg);
+}
+size_t decode_workspace(int B, int nh, int nkv) {
+  return kCounterBytes + decode_slots(B, nkv) * head_group(nkv) * (nh / nkv) * (HD + 2) * sizeof(float);
+}
+
+template <int KV, int HG, int NT>
+int launch_decode(const DecodeArgs& a, int64_t num_slots, cudaStream_t st) {
+  static bool configured = false;
+  if (!configured) {
+    const cudaError_t e = cudaFuncSetAttribute(attn_decode_kv8_kernel<KV, HG, NT>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, int(dk_smem<HG, NT>()));
+    if (e != cudaSuccess) return set_error(QW_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    configured = true;
+  }
+  // K and V as [kv head][slot][128 bytes] (64 two-byte elements: the copies move bits)
+  CUtensorMap mk, mv;
+  const uint64_t dims[3] = {64, uint64_t(num_slots), uint64_t(a.nkv)};
+  const uint64_t strides[2] = {uint64_t(a.nkv) * HD, HD};
+  const uint32_t box[3] = {64, 16, HG};
+  int rc = make_tensor_map(&mk, a.c.k, 3, dims, strides, box);
+  if (rc) return rc;
+  rc = make_tensor_map(&mv, a.c.v, 3, dims, strides, box);
+  if (rc) return rc;
+  // no more CTAs than the longest sequences could give tiles to
+  constexpr int KT = 16 * (DK_WARPS / HG);
+  int64_t tiles = (int64_t(a.max_ctx) + KT - 1) / KT;
+  if (a.window > 0)
+    tiles = std::min(tiles, (int64_t(a.window) + KT - 1) / KT + 1 + (int64_t(a.n_sink) + KT - 1) / KT);
+  const int64_t ctas = (std::max<int64_t>(tiles, 1) * a.B * a.nhg + DK_MIN_TILES - 1) / DK_MIN_TILES;
+  launch_pdl(attn_decode_kv8_kernel<KV, HG, NT>, unsigned(std::min<int64_t>(ctas, DK_CTAS)), DK_THREADS,
+             dk_smem<HG, NT>(), st, mk, mv, a);
+  return check_launch("attn_decode_kv8_kernel");
+}
+template <int KV, int HG>
+int launch_decode_nt(const DecodeArgs& a, int64_t num_slots, cudaStream_t st) {
+  return a.G <= 8 ? launch_decode<KV, HG, 1>(a, num_slots, st) : launch_decode<KV, HG, 2>(a, num_slots, st);
+}
+template <int KV>
+int launch_decode_hg(const DecodeArgs& a, int64_t num_slots, cudaStream_t st) {
+  switch (head_group(a.nkv)) {
+    case 1: return launch_decode_nt<KV, 1>(a, num_slots, st);
+    case 2: return launch_decode_nt<KV, 2>(a, num_slots, st);
+    case 4: return launch_decode_nt<KV, 4>(a, num_slots, st);
+    default: return launch_decode_nt<KV, 8>(a, num_slots, st);
+  }
+}
+
 // Checks shared by the two attention entry points.
 int check_attention(const char* who, const void* k, const void* v, const float* ks, const float* vs, int64_t num_slots,
                     int scale_block, const int32_t* table, int max_blocks, int block_size, int n_seqs, int max_context,
@@ -101,7 +683,8 @@ int check_attention(const char* who, const void* k, const void* v, const float* 
 using namespace qw;
 
 extern "C" size_t qw_attention_decode_kv8_workspace_size(int B, int max_context, int n_heads, int n_kv_heads) {
-  return B < 0 || max_context < 0 || n_heads <= 0 || n_kv_heads <= 0 ? 0 : kCounterBytes;
+  if (B < 0 || max_context < 0 || n_heads <= 0 || n_kv_heads <= 0) return 0;
+  return kv8::decode_workspace(B, n_heads, n_kv_heads);
 }
 
 extern "C" int qw_attention_decode_kv8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -124,10 +707,29 @@ extern "C" int qw_attention_decode_kv8(const void* q, const void* k_cache, const
   const size_t need = qw_attention_decode_kv8_workspace_size(B, max_context, n_heads, n_kv_heads);
   if (!workspace || workspace_bytes < need)
     return set_error(QW_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", who, need);
-  const kv8::Cache c{k_cache, v_cache, k_scale, v_scale, num_slots, kv8::scale_shift(scale_block), block_table,
-                     max_blocks, block_size};
-  return kv8::launch_attn(q, c, nullptr, context_lens, B, 1, n_heads, n_kv_heads, max_context, scale, window, n_sink, out, kv_dtype,
-                          static_cast<cudaStream_t>(stream));
+  if (!kv8::aligned16(workspace)) return set_error(QW_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", who);
+  kv8::DecodeArgs a;
+  a.q = static_cast<const bf16*>(q);
+  a.ctx = context_lens;
+  a.c = kv8::Cache{k_cache, v_cache, k_scale, v_scale, num_slots, kv8::scale_shift(scale_block), block_table, max_blocks,
+                   block_size};
+  const int hg = kv8::head_group(n_kv_heads);
+  a.B = B;
+  a.nh = n_heads;
+  a.nkv = n_kv_heads;
+  a.G = n_heads / n_kv_heads;
+  a.nhg = (n_kv_heads + hg - 1) / hg;
+  a.max_ctx = max_context;
+  a.window = window;
+  a.n_sink = n_sink;
+  a.scale_log2 = scale * kv8::kLog2e;
+  a.counters = static_cast<unsigned int*>(workspace);
+  a.ws_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterBytes);
+  a.ws_ml = a.ws_o + kv8::decode_slots(B, n_kv_heads) * hg * a.G * kv8::HD;
+  a.out = static_cast<bf16*>(out);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return kv_dtype == QW_I8 ? kv8::launch_decode_hg<QW_I8>(a, num_slots, st)
+                           : kv8::launch_decode_hg<QW_E4M3>(a, num_slots, st);
 }
 
 extern "C" size_t qw_attention_prefill_kv8_workspace_size(int n_seqs, int64_t total_q, int max_seqlen_q,

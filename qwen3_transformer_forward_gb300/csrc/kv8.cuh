@@ -94,7 +94,7 @@ inline int check_cache(const char* who, const void* k, const void* v, const floa
     return set_error(QW_ERR_DTYPE, "%s: kv_dtype %d is neither QW_I8 nor QW_E4M3", who, kv_dtype);
   if (scale_shift(scale_block) < 0)
     return set_error(QW_ERR_SHAPE, "%s: scale_block %d must be 16, 32 or 64", who, scale_block);
-  if (num_slots < 0 || num_slots > INT32_MAX)
+  if (num_slots <= 0 || num_slots > INT32_MAX)
     return set_error(QW_ERR_INVALID_ARG, "%s: num_slots %lld", who, (long long)num_slots);
   if (num_slots % scale_block)
     return set_error(QW_ERR_SHAPE, "%s: num_slots %lld is not a multiple of scale_block %d", who, (long long)num_slots,
@@ -113,6 +113,86 @@ inline int check_table(const char* who, const int32_t* table, int max_blocks, in
   (void)scale_block;   // 16, 32 or 64: divides block_size
   return QW_OK;
 }
+
+}  // namespace kv8
+}  // namespace qw
+
+// ---------------------------------------------------------------------------
+// codes as f16 pairs for the matrix instructions: every int8 and e4m3 code is
+// exact in f16.  e4m3 pairs come out times 2^-8 (code_f32_e4m3), a factor that
+// the kernels fold into the scores and the output.
+// ---------------------------------------------------------------------------
+namespace qw {
+namespace kv8 {
+
+template <int KV> __device__ constexpr float pair_factor() { return KV == QW_I8 ? 1.0f : 256.0f; }
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+// f16 pair (1024 + u0, 1024 + u1) -> (u0 - 128, u1 - 128)
+__device__ __forceinline__ uint32_t unbias(uint32_t h) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(h), "r"(0x64806480u));
+  return d;
+}
+// Codes 0, 1 and 2, 3 of word w (its codes biased by 128 for int8: w ^ 0x80808080).
+template <int KV> __device__ __forceinline__ void word_pairs(uint32_t w, uint32_t& p01, uint32_t& p23) {
+  if constexpr (KV == QW_I8) {
+    const uint32_t u = w ^ 0x80808080u;
+    p01 = unbias(prmt(u, 0x64646464u, 0x4140));   // f16 0x6400 | u = 1024 + u
+    p23 = unbias(prmt(u, 0x64646464u, 0x4342));
+  } else {   // sign-extend each byte to 16 bits, exponent and mantissa to bits 13 .. 7
+    p01 = (prmt(w, 0u, 0x9180) << 7) & 0xbf80bf80u;
+    p23 = (prmt(w, 0u, 0xb3a2) << 7) & 0xbf80bf80u;
+  }
+}
+// Codes i of words a and b side by side, i = 0 .. 3.
+template <int KV> __device__ __forceinline__ void cross_pairs(uint32_t a, uint32_t b, uint32_t (&p)[4]) {
+  if constexpr (KV == QW_I8) {
+    word_pairs<KV>(prmt(a, b, 0x5140), p[0], p[1]);
+    word_pairs<KV>(prmt(a, b, 0x7362), p[2], p[3]);
+  } else {
+    p[0] = (prmt(a, b, 0xc480) << 7) & 0xbf80bf80u;
+    p[1] = (prmt(a, b, 0xd591) << 7) & 0xbf80bf80u;
+    p[2] = (prmt(a, b, 0xe6a2) << 7) & 0xbf80bf80u;
+    p[3] = (prmt(a, b, 0xf7b3) << 7) & 0xbf80bf80u;
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Power of two that takes a row whose largest magnitude is `top` into
+// [2^14, 2^15), where its bf16 values down to 2^-28 of the largest are exact in
+// f16, and its inverse.
+__device__ __forceinline__ void row_scale(float top, float& mul, float& inv) {
+  const int e = max(int(__float_as_uint(top) >> 23), 16);     // biased exponent (bf16 rows below 2^-111: kept small)
+  mul = __uint_as_float(uint32_t(min(268 - e, 254)) << 23);   // 2^(14 - (e - 127))
+  inv = __uint_as_float(uint32_t(max(e - 14, 1)) << 23);      // 2^((e - 127) - 14)
+}
+
+// What a query at key position ctx - 1 sees of a sequence, as tiles of KT keys:
+// tiles 0 .. ns - 1 (first tokens), then w0 .. ; nt in all.
+struct Span {
+  int L, lo, w0, ns, nt;
+  __device__ __forceinline__ int tile(int t) const { return t < ns ? t : w0 + t - ns; }
+};
 
 }  // namespace kv8
 }  // namespace qw

@@ -91,6 +91,7 @@ def test_workspace_refusals(lib):
     assert need >= 64 * 1024
     for kw in (dict(ws=None), dict(wsb=need - 1), dict(wsb=0)):
         assert _call(lib, "qw_attention_decode_kv8", list(DECODE), DECODE, **kw) == WS
+    assert _call(lib, "qw_attention_decode_kv8", list(DECODE), DECODE, ws=ODD) == ARG
     # a few rows over many keys: the keys are split, and the parts need room
     need = lib.qw_attention_prefill_kv8_workspace_size(1, 4, 4, 40000, 16, 8)
     args = dict(n=1, T=4, maxq=4, mc=40000, maxb=200)
