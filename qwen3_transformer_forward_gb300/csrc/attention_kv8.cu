@@ -194,6 +194,7 @@ __global__ void __launch_bounds__(DK_THREADS, 1) attn_decode_kv8_kernel(const __
                                                                        const __grid_constant__ CUtensorMap tmV,
                                                                        const DecodeArgs a) {
   constexpr int KS = DK_WARPS / HG, KT = 16 * KS, ST = dk_stages<HG, NT>();
+  constexpr int UN = NT == 1 ? 2 : 1;                // tiles of a consumer step (two spill registers with NT 2)
   constexpr uint32_t kBox = 16 * HG * HD;            // bytes of one TMA box
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
@@ -377,25 +378,50 @@ __global__ void __launch_bounds__(DK_THREADS, 1) attn_decode_kv8_kernel(const __
       m[n][0] = m[n][1] = -INFINITY;
       l[n][0] = l[n][1] = 0.0f;
     }
-    for (int i = 0; i < n_seg; ++i, ++j, ++t) {
-      const int s = j % ST;
-      wait(full(s), uint32_t(j / ST) & 1u, 0x2u);
-      const int key0 = (sp.tile(t) * KS + ks) * 16;
-      if (head_ok && any_visible(sp, a.n_sink, key0)) {
-        const uint32_t sK = ring + uint32_t(s) * DK_STAGE + uint32_t(warp) * DK_SUB, sV = sK + DK_STAGE / 2;
-        const float sk = scales[s * 2 * DK_WARPS + warp], sv = scales[s * 2 * DK_WARPS + DK_WARPS + warp];
-        float c[NT][4];
+    // UN tiles at a time: their chains of loads, conversions and matrix instructions overlap
+    for (int i = 0; i < n_seg; i += UN, j += UN, t += UN) {
+      const bool two = UN > 1 && i + 1 < n_seg;
+      int st[UN], key0[UN];
+      bool act[UN], any = false;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.0f;
-        {
+      for (int u = 0; u < UN; ++u) {
+        st[u] = (j + u) % ST;
+        key0[u] = (sp.tile(t + u) * KS + ks) * 16;
+        act[u] = head_ok && (u == 0 || two) && any_visible(sp, a.n_sink, key0[u]);
+        any |= act[u];
+      }
+      wait(full(st[0]), uint32_t(j / ST) & 1u, 0x2u);
+      if (two) wait(full(st[UN - 1]), uint32_t((j + 1) / ST) & 1u, 0x2u);
+      if (any) {
+        float c[UN][NT][4], sk[UN], lsv[UN], isv[UN];
+        bool v_none[UN], vis[UN][2];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+          const uint32_t sK = ring + uint32_t(st[u]) * DK_STAGE + uint32_t(warp) * DK_SUB;
+          // a tile that is not there: any codes (all finite), no visible key
+          const float* sc = scales + st[u] * 2 * DK_WARPS + warp;
+          sk[u] = act[u] ? sc[0] : 0.0f;
+          const float sv = act[u] ? sc[DK_WARPS] : 1.0f;
+          v_none[u] = sv < kTinyScale;
+          const float svc = v_none[u] ? kTinyScale : sv;
+          lsv[u] = lg2(svc);
+          isv[u] = __fdividef(kUnshift, svc);
+          const bool all = key0[u] + 16 <= sp.L && (key0[u] >= sp.lo || key0[u] + 16 <= a.n_sink);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int kp = key0[u] + gq + 8 * r;
+            vis[u][r] = act[u] && (all || (kp < sp.L && (kp >= sp.lo || kp < a.n_sink)));
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) c[u][n][0] = c[u][n][1] = c[u][n][2] = c[u][n][3] = 0.0f;
           // keys gq and gq + 8, dims 32 tq .. + 31 (16-byte chunks 2 tq, 2 tq + 1)
           uint32_t k0[8], k1[8];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint32_t at = sK + uint32_t(gq) * 128u + (uint32_t((2 * tq + u) ^ gq) << 4);
+          for (int w = 0; w < 2; ++w) {
+            const uint32_t at = sK + uint32_t(gq) * 128u + (uint32_t((2 * tq + w) ^ gq) << 4);
             const uint4 x = lds128(at), y = lds128(at + 1024u);
-            k0[4 * u] = x.x; k0[4 * u + 1] = x.y; k0[4 * u + 2] = x.z; k0[4 * u + 3] = x.w;
-            k1[4 * u] = y.x; k1[4 * u + 1] = y.y; k1[4 * u + 2] = y.z; k1[4 * u + 3] = y.w;
+            k0[4 * w] = x.x; k0[4 * w + 1] = x.y; k0[4 * w + 2] = x.z; k0[4 * w + 3] = x.w;
+            k1[4 * w] = y.x; k1[4 * w + 1] = y.y; k1[4 * w + 2] = y.z; k1[4 * w + 3] = y.w;
           }
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
@@ -403,52 +429,47 @@ __global__ void __launch_bounds__(DK_THREADS, 1) attn_decode_kv8_kernel(const __
             word_pairs<KV>(k0[kk], a0, a2);
             word_pairs<KV>(k1[kk], a1, a3);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16(c[n], a0, a1, a2, a3, qb[n][kk][0], qb[n][kk][1]);
+            for (int n = 0; n < NT; ++n) mma_f16(c[u][n], a0, a1, a2, a3, qb[n][kk][0], qb[n][kk][1]);
           }
         }
-        // V: keys 2 tq, 2 tq + 1 and the same + 8, dims 16 gq .. + 15
-        uint4 v[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int r = 2 * tq + (u & 1) + 8 * (u >> 1);
-          v[u] = lds128(sV + uint32_t(r) * 128u + (uint32_t(gq ^ (r & 7)) << 4));
-        }
-        const bool v_none = sv < kTinyScale;
-        const float svc = v_none ? kTinyScale : sv;
-        const float lsv = lg2(svc), isv = __fdividef(kUnshift, svc);
-        const bool all = key0 + 16 <= sp.L && (key0 >= sp.lo || key0 + 16 <= a.n_sink);
-        bool vis[2] = {true, true};
-        if (!all) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int kp = key0 + gq + 8 * u;
-            vis[u] = kp < sp.L && (kp >= sp.lo || kp < a.n_sink);
-          }
-        }
-        uint32_t pb[NT][2];
+        uint32_t pb[UN][NT][2];
         bool grew = false;
         float al[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          float p[4];
+          float p[UN][4];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float f = qa[n][e] * sk;
-            const float x0 = vis[0] ? fmaf(c[n][e], f, lsv) : -INFINITY, x1 = vis[1] ? fmaf(c[n][e + 2], f, lsv) : -INFINITY;
-            float mx = fmaxf(x0, x1);
+            float x[UN][2], mx = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < UN; ++u) {
+              const float f = qa[n][e] * sk[u];
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                x[u][r] = vis[u][r] ? fmaf(c[u][n][e + 2 * r], f, lsv[u]) : -INFINITY;
+                mx = fmaxf(mx, x[u][r]);
+              }
+            }
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float m_new = fmaxf(m[n][e], mx);
+            const float m_new = fmaxf(m[n][e], mx);   // finite: a key of these tiles is visible
             grew |= m_new > m[n][e];
-            al[n][e] = ex2(m[n][e] - m_new);   // (a visible key is in the tile: m_new is finite)
+            al[n][e] = ex2(m[n][e] - m_new);
             m[n][e] = m_new;
-            p[e] = ex2(x0 - m_new + kShift);
-            p[e + 2] = ex2(x1 - m_new + kShift);
-            l[n][e] = fmaf(l[n][e], al[n][e], (p[e] + p[e + 2]) * isv);
+            l[n][e] *= al[n][e];
+#pragma unroll
+            for (int u = 0; u < UN; ++u) {   // (x - m first: both may be huge, the difference of the largest is exactly zero)
+              p[u][e] = ex2(x[u][0] - m_new + kShift);
+              p[u][e + 2] = ex2(x[u][1] - m_new + kShift);
+              l[n][e] = fmaf(p[u][e] + p[u][e + 2], isv[u], l[n][e]);
+            }
           }
-          pb[n][0] = transpose8(v_none ? 0u : pack_f16(p[0], p[1]));   // keys 2 tq, + 1 of head gq
-          pb[n][1] = transpose8(v_none ? 0u : pack_f16(p[2], p[3]));   // keys 8 + 2 tq, + 1
+#pragma unroll
+          for (int u = 0; u < UN; ++u) {
+            pb[u][n][0] = transpose8(v_none[u] ? 0u : pack_f16(p[u][0], p[u][1]));   // keys 2 tq, + 1 of head gq
+            pb[u][n][1] = transpose8(v_none[u] ? 0u : pack_f16(p[u][2], p[u][3]));   // keys 8 + 2 tq, + 1
+          }
         }
         if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -461,22 +482,41 @@ __global__ void __launch_bounds__(DK_THREADS, 1) attn_decode_kv8_kernel(const __
               o[n][d][3] *= al[n][1];
             }
         }
-        // O^T rows: tile d holds dims 16 gq + 2 d (row gq) and 16 gq + 2 d + 1 (row gq + 8)
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t* vw[4] = {&v[0].x + w, &v[1].x + w, &v[2].x + w, &v[3].x + w};
-          uint32_t lo4[4], hi4[4];
-          cross_pairs<KV>(*vw[0], *vw[1], lo4);
-          cross_pairs<KV>(*vw[2], *vw[3], hi4);
+        for (int u = 0; u < UN; ++u) {
+          // V: keys 2 tq, 2 tq + 1 and the same + 8, dims 16 gq .. + 15
+          const uint32_t sV = ring + uint32_t(st[u]) * DK_STAGE + DK_STAGE / 2 + uint32_t(warp) * DK_SUB;
+          uint32_t v[4][4];
 #pragma unroll
-          for (int d = 0; d < 2; ++d)
+          for (int r = 0; r < 4; ++r) {
+            const int row = 2 * tq + (r & 1) + 8 * (r >> 1);
+            const uint4 x = lds128(sV + uint32_t(row) * 128u + (uint32_t(gq ^ (row & 7)) << 4));
+            v[r][0] = x.x; v[r][1] = x.y; v[r][2] = x.z; v[r][3] = x.w;
+          }
+          // O^T rows: tile d holds dims 16 gq + 2 d (row gq) and 16 gq + 2 d + 1 (row gq + 8)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-              mma_f16(o[n][2 * w + d], lo4[2 * d], lo4[2 * d + 1], hi4[2 * d], hi4[2 * d + 1], pb[n][0], pb[n][1]);
+          for (int w = 0; w < 4; ++w) {
+            uint32_t lo4[4], hi4[4];
+            cross_pairs<KV>(v[0][w], v[1][w], lo4);
+            cross_pairs<KV>(v[2][w], v[3][w], hi4);
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma_f16(o[n][2 * w + d], lo4[2 * d], lo4[2 * d + 1], hi4[2 * d], hi4[2 * d + 1], pb[u][n][0],
+                        pb[u][n][1]);
+          }
         }
       }
       __syncwarp();
-      if (lane == 0) tcx::mbar_arrive(empty(s));
+      if (lane == 0) {
+        tcx::mbar_arrive(empty(st[0]));
+        if (two) tcx::mbar_arrive(empty(st[UN - 1]));
+      }
+      if (UN > 1 && !two) {   // the part's last tile stood alone
+        --j;
+        --t;
+      }
     }
     // ---- end of this CTA's part of the pair: sums over the lanes of a head, then over the head's warps
 #pragma unroll
@@ -567,37 +607,55 @@ __global__ void __launch_bounds__(DK_THREADS, 1) attn_decode_kv8_kernel(const __
         before = __shfl_sync(0xffffffffu, before, 0);
         if (before == unsigned(c_last - c_first)) {
           __threadfence();
-          for (int hd = 0; hd < a.G; ++hd) {
-            auto index = [&](int c) { return ((int64_t(c) + pair) * HG + h) * a.G + hd; };
-            float M = -INFINITY;
-            for (int c = c_first + lane; c <= c_last; c += 32) M = fmaxf(M, __ldcg(a.ws_ml + 2 * index(c)));
-            M = warp_max(M);
-            const float mu = M == -INFINITY ? 0.0f : M;
-            float lsum = 0.0f;
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int c0 = c_first; c0 <= c_last; c0 += 8) {
-              float wgt[8], lc[8];
-              float4 x[8];
+          // four heads at a time, four CTAs' parts each: 32 loads in flight for a lane
+          for (int h0 = 0; h0 < a.G; h0 += 4) {
+            auto index = [&](int c, int u) { return ((int64_t(c) + pair) * HG + h) * a.G + min(h0 + u, a.G - 1); };
+            float M[4], lsum[4];
+            float4 acc[4];
 #pragma unroll
-              for (int u = 0; u < 8; ++u) {   // one batch of loads in flight together
-                const int64_t idx = index(min(c0 + u, c_last));
-                const bool in = c0 + u <= c_last;
-                wgt[u] = in ? ex2(__ldcg(a.ws_ml + 2 * idx) - mu) : 0.0f;
-                lc[u] = __ldcg(a.ws_ml + 2 * idx + 1);
-                x[u] = __ldcg(reinterpret_cast<const float4*>(a.ws_o + idx * HD) + lane);
-              }
-#pragma unroll
-              for (int u = 0; u < 8; ++u) {
-                lsum = fmaf(lc[u], wgt[u], lsum);
-                acc.x = fmaf(x[u].x, wgt[u], acc.x);
-                acc.y = fmaf(x[u].y, wgt[u], acc.y);
-                acc.z = fmaf(x[u].z, wgt[u], acc.z);
-                acc.w = fmaf(x[u].w, wgt[u], acc.w);
-              }
+            for (int u = 0; u < 4; ++u) {
+              M[u] = -INFINITY;
+              lsum[u] = 0.0f;
+              acc[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
-            const float fac = lsum > 0.0f ? kUnshift * pair_factor<KV>() / lsum : 0.0f;
-            *reinterpret_cast<uint2*>(a.out + (int64_t(b) * a.nh + g * a.G + hd) * HD + 4 * lane) =
-                make_uint2(pack_bf16(acc.x * fac, acc.y * fac), pack_bf16(acc.z * fac, acc.w * fac));
+            for (int c = c_first + lane; c <= c_last; c += 32)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) M[u] = fmaxf(M[u], __ldcg(a.ws_ml + 2 * index(c, u)));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              M[u] = warp_max(M[u]);
+              if (M[u] == -INFINITY) M[u] = 0.0f;
+            }
+            for (int c0 = c_first; c0 <= c_last; c0 += 4) {
+              float2 ml[4][4];
+              float4 x[4][4];
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  const int64_t idx = index(min(c0 + v, c_last), u);
+                  ml[v][u] = __ldcg(reinterpret_cast<const float2*>(a.ws_ml) + idx);
+                  x[v][u] = __ldcg(reinterpret_cast<const float4*>(a.ws_o + idx * HD) + lane);
+                }
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  const float w = c0 + v <= c_last ? ex2(ml[v][u].x - M[u]) : 0.0f;
+                  lsum[u] = fmaf(ml[v][u].y, w, lsum[u]);
+                  acc[u].x = fmaf(x[v][u].x, w, acc[u].x);
+                  acc[u].y = fmaf(x[v][u].y, w, acc[u].y);
+                  acc[u].z = fmaf(x[v][u].z, w, acc[u].z);
+                  acc[u].w = fmaf(x[v][u].w, w, acc[u].w);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              if (h0 + u >= a.G) continue;
+              const float fac = lsum[u] > 0.0f ? kUnshift * pair_factor<KV>() / lsum[u] : 0.0f;
+              *reinterpret_cast<uint2*>(a.out + (int64_t(b) * a.nh + g * a.G + h0 + u) * HD + 4 * lane) =
+                  make_uint2(pack_bf16(acc[u].x * fac, acc[u].y * fac), pack_bf16(acc[u].z * fac, acc[u].w * fac));
+            }
           }
           if (lane == 0) a.counters[b * a.nkv + g] = 0u;
         }
