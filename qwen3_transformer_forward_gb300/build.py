@@ -20,7 +20,8 @@ LIB = PKG / "libqw.so"
 BUILD_DIR = ROOT / "_build"
 
 SOURCES = ["qw_api.cu", "elementwise.cu", "gemm.cu", "attention.cu", "attention_prefill.cu", "decode_step.cu",
-           "sampler.cu", "kv8_cache.cu", "attention_kv8.cu"]
+           "sampler.cu", "kv8_cache.cu", "attention_kv8.cu",
+           "attention_kv8_prefill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-warn-spills"]

@@ -1,0 +1,709 @@
+// Causal varlen prefill attention over the 8-bit paged KV cache on tcgen05
+// tensor cores, with a sliding window and first tokens that stay visible.
+//
+// The query rows of one kv head are packed: row R of a sequence is token R / G,
+// q head R % G of its group of G, so that any group size fills the 128-row units
+// and a short prompt wastes few rows.  One CTA owns two units (256 rows) and
+// walks the key tiles (128 keys) that any of its rows sees.  Per CTA (16 warps):
+//   warp 0        allocates 512 TMEM columns and issues every MMA from one thread:
+//                   S_u  = Q_u K_j^T   A = Q_u (smem), B = K_j (smem), both K-major
+//                   O_u += P_u V_j     A = P_u (TMEM), B = V_j (smem, MN-major)
+//                 in the order PV_0(j), S_0(j+1), PV_1(j), S_1(j+1)
+//   warps 4-7     read the codes of K_j and V_j from the cache into registers one
+//                 tile ahead, convert them to f16 (exact) and store them as
+//                 128-byte-swizzled operand tiles, two slots each: 1.25 to 1.5
+//                 instructions an element, once for the 256 rows of both units
+//   warps 8-11    softmax of unit 0, warps 12-15 of unit 1: one row per thread
+// Block scales never touch the operands.  A block of 16 keys shares one scale,
+// so with x = score * log2 e * k_scale + log2(v_scale) the running maximum m is
+// over x, P = 2^(x - m + 7) is rounded to f16 (11 bits; m is raised lazily, when a
+// row's maximum grows by more than 2^8, so that P <= 2^15), O takes the codes of
+// V alone and the denominator is sum 2^(x - m) / v_scale in fp32.  q is moved by a
+// power of two per row (row_scale), exact in f16.  k_scale >= 0 and the softmax
+// scale's sign sits in q, so a block's largest x belongs to its largest score:
+// the maximum is taken over the raw scores.
+// TMEM columns: S_0/P_0 [0,128), S_1/P_1 [128,256), O_0 [256,384), O_1 [384,512).
+// Few rows over many keys: the tiles are cut into `splits` shares (host rule in
+// prefill_splits), each CTA leaves (m, l, O) in fp32 and a second kernel adds them
+// in order.
+// Every mbarrier wait is bounded (2 s); on timeout the kernel records an error
+// word and runs to its end without waiting further.
+#include <math.h>
+
+#include <algorithm>
+
+#include "kv8.cuh"
+#include "tc_common.cuh"
+
+namespace qw {
+namespace kv8p {
+
+using namespace kv8;
+
+__device__ unsigned int g_kv8_prefill_error = 0;
+
+constexpr int BM = 128, BN = 128, ROWS = 2 * BM, THREADS = 512;
+constexpr uint32_t BOX = 16384;                    // 128 rows x 64 f16
+constexpr uint32_t TILE = 2 * BOX;                 // 128 rows x 128 f16
+constexpr uint32_t OFF_Q = 0;                      // Q_0, Q_1 (then the output staging)
+constexpr uint32_t OFF_K = 2 * TILE;               // K_j in slot j % 2
+constexpr uint32_t OFF_V = 4 * TILE;
+constexpr uint32_t OFF_SCL = 6 * TILE;             // [4 tiles][8 blocks] {k_scale, log2 v_scale, 2^-7 / v_scale, -}
+constexpr uint32_t OFF_BAR = OFF_SCL + 4 * 8 * 16;
+constexpr size_t SMEM = 1024 + OFF_BAR + 256;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleLog2 = 8.0f, kShift = 7.0f, kUnshift = 1.0f / 128.0f;
+// Past this |m| the exponent is formed as (x - m) + 7 instead of one fused step,
+// whose constant log2(v_scale) - m + 7 would be rounded too coarsely.
+constexpr float kBigScore = 512.0f;
+
+constexpr int B_K_FULL = 0, B_K_EMPTY = 2, B_V_FULL = 4, B_V_EMPTY = 6, B_Q = 8, B_S_FULL = 10, B_P_FULL = 12,
+              B_O_DONE = 14, B_DONE = 16, N_BARS = 17;
+static_assert(N_BARS * 8 + 4 <= 256, "barrier area");
+
+// kind::f16 instruction descriptor with f16 A and B, fp32 D
+constexpr uint32_t idesc_f16(int M, int N) { return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24); }
+constexpr uint32_t IDESC_S = idesc_f16(BM, BN);
+constexpr uint32_t IDESC_PV = idesc_f16(BM, HD) | tcx::kIdescBMajorMN;
+
+__device__ __forceinline__ uint32_t tile_off(int r, int c) {   // row r, 16-byte chunk c of 16
+  return uint32_t(c >> 3) * BOX + uint32_t(r) * 128u + (uint32_t((c & 7) ^ (r & 7)) << 4);
+}
+__device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+template <int N> __device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+// Registers at launch: 128 a thread.  4 warpgroups: 40 + 104 + 184 + 184 = 4 * 128.
+constexpr int kRegsIssue = 40, kRegsConvert = 104, kRegsSoftmax = 184;
+static_assert(kRegsIssue + kRegsConvert + 2 * kRegsSoftmax <= 4 * 128, "register pool of one CTA");
+
+__device__ __forceinline__ uint64_t pair64(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpair64(uint64_t p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+struct PrefillArgs {
+  const bf16* q;
+  Cache c;
+  const int32_t* cu_q;
+  const int32_t* ctx;
+  int64_t total_q;
+  int max_q, max_ctx, nh, nkv, G, window, n_sink, splits;
+  float scale_log2;     // |scale| log2 e
+  float q_sign;         // sign of the scale
+  bf16* out;
+  float* ws_o;          // [splits][total_q * nh][128]
+  float* ws_ml;         // [splits][total_q * nh][2]
+};
+
+// Rows of one CTA (or one row of the merge): the sequence's packed rows from R0.
+struct Rows {
+  int qs, lq, start, n;   // first token, new tokens, key position of token 0, packed rows that exist
+  __device__ __forceinline__ int64_t id(const PrefillArgs& a, int R, int g) const {   // row of q and out
+    return (int64_t(qs) + R / a.G) * a.nh + g * a.G + R % a.G;
+  }
+};
+__device__ __forceinline__ Rows rows_of(const PrefillArgs& a, int s) {
+  Rows r;
+  r.qs = a.cu_q[s];
+  r.lq = a.cu_q[s + 1] - r.qs;
+  r.start = a.ctx[s] - r.lq;
+  int tok = min(r.lq, a.max_q);
+  if (r.qs < 0 || int64_t(r.qs) + tok > a.total_q) tok = 0;
+  r.n = max(tok, 0) * a.G;
+  return r;
+}
+
+template <int KV>
+__global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const PrefillArgs a) {
+  pdl_wait();      // inputs of this kernel are complete and visible
+  pdl_trigger();   // only now may the next kernel start its prologue
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(sm);
+  auto bar = [&](int i) { return sbase + OFF_BAR + 8u * uint32_t(i); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + OFF_BAR + N_BARS * 8);
+  const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
+
+  const int s = blockIdx.z, g = blockIdx.y;
+  const int n_x = int(gridDim.x) / a.splits;
+  const int split = int(blockIdx.x) % a.splits;
+  const int R0 = (n_x - 1 - int(blockIdx.x) / a.splits) * ROWS;   // longest (causal) rows first
+  const Rows rw = rows_of(a, s);
+  if (R0 >= rw.n) return;   // uniform over the CTA, before any barrier or TMEM use
+  if (a.ctx[s] > a.max_ctx && threadIdx.x == 0) atomicOr(&g_kv8_prefill_error, kErrContextOverflow);
+  // key tiles that any row sees: 0 .. ns - 1 (first tokens), then w0 .. ; unit u needs the first n_u of the list
+  const int cap = min(a.ctx[s], a.max_ctx);                       // keys past it are not read
+  const int p_lo = rw.start + R0 / a.G;                           // key position of the CTA's first row
+  const int lo_cta = a.window > 0 ? max(p_lo + 1 - a.window, 0) : 0;
+  const int w0 = lo_cta / BN;
+  const int ns = min((min(a.n_sink, lo_cta) + BN - 1) / BN, w0);
+  int n_u[2], hi_cta = 0;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int last = min(R0 + BM * u + BM, rw.n) - 1;             // the unit's last row
+    const int hi = last >= R0 + BM * u ? min(rw.start + last / a.G + 1, cap) : 0;   // keys its rows see end here
+    hi_cta = max(hi_cta, hi);
+    const int tb = hi > 0 ? (hi + BN - 1) / BN : 0;
+    n_u[u] = tb > w0 ? ns + tb - w0 : min(ns, tb);
+  }
+  const int n_all = max(n_u[0], n_u[1]);
+  const int t0 = int(int64_t(n_all) * split / a.splits), t1 = int(int64_t(n_all) * (split + 1) / a.splits);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) n_u[u] = max(min(n_u[u], t1) - t0, 0);
+  const int n_kv = max(n_u[0], n_u[1]);
+  auto tile_key = [&](int j) { return (t0 + j < ns ? t0 + j : w0 + t0 + j - ns) * BN; };   // first key of tile j
+  const int64_t n_rows_all = a.total_q * a.nh;
+
+  // rows without a tile: zero output, or an empty part
+  auto no_tiles = [&](int R, int n, int t, int step) {
+    for (int i = t; i < n * 16; i += step) {
+      const int row = R + i / 16, c = i % 16;
+      if (row >= rw.n) break;
+      const int64_t id = rw.id(a, row, g);
+      if (a.splits == 1) {
+        *reinterpret_cast<uint4*>(a.out + id * HD + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
+      } else if (c == 0) {
+        a.ws_ml[2 * (split * n_rows_all + id)] = -INFINITY;
+        a.ws_ml[2 * (split * n_rows_all + id) + 1] = 0.0f;
+      }
+    }
+  };
+  if (n_kv == 0) {
+    no_tiles(R0, ROWS, threadIdx.x, THREADS);
+    return;   // uniform over the CTA
+  }
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tcx::mbar_init(bar(B_K_FULL + i), 4);
+      tcx::mbar_init(bar(B_K_EMPTY + i), 1);
+      tcx::mbar_init(bar(B_V_FULL + i), 4);
+      tcx::mbar_init(bar(B_V_EMPTY + i), 1);
+      tcx::mbar_init(bar(B_Q + i), BM);
+      tcx::mbar_init(bar(B_S_FULL + i), 1);
+      tcx::mbar_init(bar(B_P_FULL + i), 4);
+      tcx::mbar_init(bar(B_O_DONE + i), 1);
+    }
+    tcx::mbar_init(bar(B_DONE), 1);
+    tcx::fence_mbar_init();
+  }
+  if (warp == 0) {
+    tcx::tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+    tcx::tmem_relinquish();
+  }
+  tcx::tc_fence_before();
+  __syncthreads();
+  tcx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool ok = true;
+  auto wait = [&](int b, uint32_t parity, uint32_t code) {
+    if (ok && !tcx::mbar_wait(bar(b), parity, &g_kv8_prefill_error, 1u << code)) ok = false;
+  };
+
+  if (warp < 4) {
+    regs_less<kRegsIssue>();
+    // ---------------- MMA issuer (one thread) ----------------
+    if (warp == 0 && lane == 0) {
+      auto issue_s = [&](int u, int j) {   // S_u(j) = Q_u K_j^T
+        const uint32_t qaddr = sbase + OFF_Q + uint32_t(u) * TILE;
+        const uint32_t kaddr = sbase + OFF_K + uint32_t(j & 1) * TILE;
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk) {
+          const uint32_t off = uint32_t(kk >> 2) * BOX + uint32_t(kk & 3) * 32u;
+          umma_ss(tmem + uint32_t(u) * 128u, tcx::sw128_desc(qaddr + off), tcx::sw128_desc(kaddr + off), IDESC_S,
+                  kk > 0 ? 1u : 0u);
+        }
+        tcx::umma_commit(bar(B_S_FULL + u));
+      };
+      auto issue_pv = [&](int u, int j) {   // O_u += P_u V_j
+        const uint32_t vaddr = sbase + OFF_V + uint32_t(j & 1) * TILE;
+        const uint32_t tS = tmem + uint32_t(u) * 128u;
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk)
+          umma_ts(tS + 256u, tS + uint32_t(kk) * 8u, tcx::sw128_desc_mn(vaddr + uint32_t(kk) * 2048u, BOX), IDESC_PV,
+                  (j > 0 || kk > 0) ? 1u : 0u);
+        tcx::umma_commit(bar(B_O_DONE + u));
+      };
+      if (n_u[0] > 0) wait(B_Q, 0u, 5u);
+      if (n_u[1] > 0) wait(B_Q + 1, 0u, 5u);
+      wait(B_K_FULL, 0u, 6u);
+      tcx::tc_fence_after();
+      if (n_u[0] > 0) issue_s(0, 0);
+      if (n_u[1] > 0) issue_s(1, 0);
+      tcx::umma_commit(bar(B_K_EMPTY));   // K_0 released once both S(0) complete
+      for (int j = 0; j < n_kv; ++j) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (j < n_u[u]) {
+            // P_u(j) written; its softmax also saw V_j (and K_{j+1}) land
+            wait(B_P_FULL + u, uint32_t(j) & 1u, 8u);
+            tcx::tc_fence_after();
+            issue_pv(u, j);
+            if (j + 1 < n_u[u]) {
+              // S_u(j+1) overwrites the P_u(j) that PV_u(j) reads
+              wait(B_O_DONE + u, uint32_t(j) & 1u, 10u);
+              tcx::tc_fence_after();
+              issue_s(u, j + 1);
+            }
+          }
+        }
+        tcx::umma_commit(bar(B_V_EMPTY + (j & 1)));
+        if (j + 1 < n_kv) tcx::umma_commit(bar(B_K_EMPTY + ((j + 1) & 1)));
+      }
+      // every MMA of this CTA has completed before TMEM is released
+      tcx::umma_commit(bar(B_DONE));
+      wait(B_DONE, 0u, 11u);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    regs_less<kRegsConvert>();
+    // ---------------- converters: warp w holds keys 32 w .. + 31 of every tile ----------------
+    const int w = warp - 4, rsub = lane >> 2, c4 = lane & 3;
+    const int64_t row_bytes = int64_t(a.nkv) * HD;
+    uint4 kr[8], vr[8];
+    float sk = 0.0f, sv = 0.0f;            // lanes 0, 1: scales of the warp's two blocks
+    int64_t row0 = -1;                     // cache row of the warp's first key
+    bool has[2] = {false, false};          // its two blocks are seen by some row and have a page
+    auto find = [&](int j) {
+      const int key0 = tile_key(j) + 32 * w;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int k = key0 + 16 * b;
+        has[b] = max(k, lo_cta) < min(k + 16, hi_cta) || k < min(a.n_sink, hi_cta);
+      }
+      row0 = has[0] || has[1] ? row_of(a.c.table, a.c.max_blocks, a.c.block_size, a.c.num_slots, s, key0) : -1;
+      if (row0 < 0) has[0] = has[1] = false;
+      if (row0 + 16 >= a.c.num_slots) has[1] = false;   // (the cache may end inside a page, after a whole block)
+    };
+    auto load = [&](uint4 (&x)[8], const void* cache) {
+      const uint8_t* base = static_cast<const uint8_t*>(cache) + (row0 + rsub) * row_bytes + int64_t(g) * HD + 16 * c4;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          x[2 * k + b] = has[k >> 1] ? __ldg(reinterpret_cast<const uint4*>(base + 8 * k * row_bytes + 64 * b))
+                                     : make_uint4(0u, 0u, 0u, 0u);
+    };
+    auto load_scales = [&]() {
+      sk = sv = 0.0f;
+      if (lane < 2 && (lane ? has[1] : has[0])) {
+        const int64_t at = ((row0 + 16 * lane) >> a.c.sb_shift) * a.nkv + g;
+        sk = a.c.k_scale[at];
+        sv = a.c.v_scale[at];
+      }
+    };
+    auto store = [&](const uint4 (&x)[8], uint32_t off) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          uint8_t* dst = sm + off + uint32_t(b) * BOX + uint32_t(32 * w + 8 * k + rsub) * 128u;
+          const uint4 y = x[2 * k + b];
+          uint4 lo, hi;
+          word_pairs<KV>(y.x, lo.x, lo.y);
+          word_pairs<KV>(y.y, lo.z, lo.w);
+          word_pairs<KV>(y.z, hi.x, hi.y);
+          word_pairs<KV>(y.w, hi.z, hi.w);
+          *reinterpret_cast<uint4*>(dst + (((2 * c4) ^ rsub) << 4)) = lo;
+          *reinterpret_cast<uint4*>(dst + (((2 * c4 + 1) ^ rsub) << 4)) = hi;
+        }
+    };
+    auto publish = [&](int b) {
+      tcx::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) tcx::mbar_arrive(bar(b));
+    };
+    find(0);
+    load_scales();
+    load(kr, a.c.k);
+    load(vr, a.c.v);
+    for (int j = 0; j < n_kv; ++j) {
+      const int slot = j & 1;
+      bool zero_v[2];   // blocks whose v_scale counts as zero
+#pragma unroll
+      for (int b = 0; b < 2; ++b) zero_v[b] = !(__shfl_sync(0xffffffffu, sv, b) >= kTinyScale);
+      const bool seen = lane ? has[1] : has[0];
+      const int key0 = tile_key(j) + 32 * w + 16 * (lane & 1);
+      // a block without a page counts as zero keys; one that no row sees is left out
+      const bool act = max(key0, lo_cta) < min(key0 + 16, hi_cta) || key0 < min(a.n_sink, hi_cta);
+      if (j >= 2) wait(B_K_EMPTY + slot, uint32_t((j >> 1) - 1) & 1u, 1u);
+      if (lane < 2) {
+        const float svc = fmaxf(seen ? sv : 0.0f, kTinyScale);
+        *reinterpret_cast<float4*>(sm + OFF_SCL + ((j & 3) * 8 + 2 * w + lane) * 16) =
+            act ? make_float4(seen ? sk : 0.0f, lg2(svc), __fdividef(kUnshift, svc), 0.0f)
+                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+      store(kr, OFF_K + uint32_t(slot) * TILE);
+      publish(B_K_FULL + slot);
+      if (j + 1 < n_kv) {
+        find(j + 1);
+        load_scales();
+        load(kr, a.c.k);
+      }
+      if (j >= 2) wait(B_V_EMPTY + slot, uint32_t((j >> 1) - 1) & 1u, 2u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (zero_v[i >> 2]) vr[i] = make_uint4(0u, 0u, 0u, 0u);
+      store(vr, OFF_V + uint32_t(slot) * TILE);
+      publish(B_V_FULL + slot);
+      if (j + 1 < n_kv) load(vr, a.c.v);
+    }
+  } else {
+    regs_more<kRegsSoftmax>();
+    // ---------------- softmax (one query row per thread) ----------------
+    const int u = (warp - 8) >> 2;
+    const int quarter = warp & 3;             // TMEM lanes this warp may access
+    const int r = quarter * 32 + lane;        // row within the unit
+    const int nu = u ? n_u[1] : n_u[0];
+    const int Ru = R0 + BM * u;
+    uint8_t* sQ = sm + OFF_Q + u * TILE;
+    if (nu == 0) {
+      no_tiles(Ru, BM, r, BM);
+    } else {
+      const bool valid = Ru + r < rw.n;
+      const int64_t id = rw.id(a, valid ? Ru + r : Ru, g);
+      float rowf;
+      {
+        uint4 x[16];
+        float top = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          x[c] = valid ? *reinterpret_cast<const uint4*>(a.q + id * HD + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t wd[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(wd[e])), fabsf(bf16_hi(wd[e]))));
+        }
+        float mul, inv;
+        row_scale(top, mul, inv);
+        mul *= a.q_sign;
+        rowf = inv * a.scale_log2 * pair_factor<KV>();
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          auto cv = [&](uint32_t v) { return pack_f16(bf16_lo(v) * mul, bf16_hi(v) * mul); };
+          *reinterpret_cast<uint4*>(sQ + tile_off(r, c)) = make_uint4(cv(x[c].x), cv(x[c].y), cv(x[c].z), cv(x[c].w));
+        }
+      }
+      // The first tile's scales.  Waited for before this thread lets S(0) start: the slot is
+      // filled again only after S(0), so this phase cannot be missed.
+      wait(B_K_FULL, 0u, 14u);
+      tcx::fence_proxy_async();
+      tcx::mbar_arrive(bar(B_Q + u));
+
+      const int p = rw.start + (Ru + r) / a.G;              // key position of this row
+      const int hi = valid ? min(p + 1, cap) : 0;           // it sees keys lo_row .. hi - 1 and 0 .. n_sink - 1 below hi
+      const int lo_row = a.window > 0 ? max(p + 1 - a.window, 0) : 0;
+      const uint32_t tS = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(u) * 128u;
+      const uint32_t tO = tS + 256u;
+      float m = -INFINITY, l = 0.0f;
+      for (int j = 0; j < nu; ++j) {
+        // S_u(j) complete, and with it every earlier MMA (O_u holds PV_u(j-1))
+        wait(B_S_FULL + u, uint32_t(j) & 1u, 12u);
+        tcx::tc_fence_after();
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tcx::tmem_ld32(tS + 32u * c, sr[c]);
+        tcx::tmem_ld_wait();
+        const int k0 = tile_key(j);
+        const bool whole = k0 + BN <= hi && (k0 >= lo_row || k0 + BN <= a.n_sink);
+        if (!whole) {
+          const int end = hi - k0, beg = lo_row - k0, snk = a.n_sink - k0;   // columns [beg, end) and [0, min(snk, end))
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int col = 32 * c + e;
+              if (!(col < end && (col >= beg || col < snk))) sr[c][e] = __float_as_uint(-INFINITY);
+            }
+        }
+        const float4* scl = reinterpret_cast<const float4*>(sm + OFF_SCL) + (j & 3) * 8;
+        float fb[8], lb[8], m_tile = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          const uint32_t* x = &sr[b >> 1][16 * (b & 1)];
+          float mx0 = __uint_as_float(x[0]), mx1 = __uint_as_float(x[1]);
+#pragma unroll
+          for (int e = 2; e < 16; e += 2) {
+            mx0 = fmaxf(mx0, __uint_as_float(x[e]));
+            mx1 = fmaxf(mx1, __uint_as_float(x[e + 1]));
+          }
+          const float mx = fmaxf(mx0, mx1);
+          const float4 sc = scl[b];
+          fb[b] = rowf * sc.x;
+          lb[b] = sc.y;
+          // (a block without a visible key: -inf, whatever the factor)
+          m_tile = fmaxf(m_tile, mx == -INFINITY ? -INFINITY : fmaf(mx, fb[b], lb[b]));
+        }
+        float alpha = 1.0f;
+        bool rescale = false;
+        if (m_tile > m + kRescaleLog2) {
+          alpha = ex2(m - m_tile);
+          m = m_tile;
+          rescale = true;
+        }
+        const float m_use = m == -INFINITY ? 0.0f : m;
+        l *= alpha;
+        const bool big = __any_sync(0xffffffffu, fabsf(m_use) > kBigScore);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const int b = 4 * c + h;
+            uint32_t* x = &sr[b >> 1][16 * (b & 1)];
+            uint64_t sum = 0;
+            const float cb = lb[b] - m_use + kShift;
+            const uint64_t f2 = pair64(fb[b], fb[b]), c2 = pair64(cb, cb);
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              float x0 = __uint_as_float(x[e]), x1 = __uint_as_float(x[e + 1]);
+              if (big || !whole) {   // (a factor of zero times -inf is NaN: masked columns stay -inf)
+                x0 = x0 == -INFINITY ? x0 : fmaf(x0, fb[b], lb[b]) - m_use + kShift;
+                x1 = x1 == -INFINITY ? x1 : fmaf(x1, fb[b], lb[b]) - m_use + kShift;
+              } else {
+                unpair64(fma2(pair64(x0, x1), f2, c2), x0, x1);
+              }
+              const float p0 = ex2(x0), p1 = ex2(x1);
+              sum = add2(sum, pair64(p0, p1));
+              pk[8 * h + e / 2] = pack_f16(p0, p1);
+            }
+            float s0, s1;
+            unpair64(sum, s0, s1);
+            l = fmaf(s0 + s1, scl[b].z, l);
+          }
+          tcx::tmem_st32(tS + 32u * c, pk);   // P_u(j): keys 64 c .. + 63
+        }
+        if (j >= 1 && __any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tcx::tmem_ld32(tO + 32u * c, o);
+            tcx::tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tcx::tmem_st32(tO + 32u * c, o);
+          }
+        }
+        tcx::tmem_st_wait();
+        // the MMA thread issues PV_u(j) and S_u(j+1) on this signal alone
+        wait(B_V_FULL + (j & 1), uint32_t(j >> 1) & 1u, 14u);
+        if (j + 1 < nu) wait(B_K_FULL + ((j + 1) & 1), uint32_t((j + 1) >> 1) & 1u, 14u);
+        tcx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tcx::mbar_arrive(bar(B_P_FULL + u));
+      }
+      wait(B_O_DONE + u, uint32_t(nu - 1) & 1u, 13u);
+      tcx::tc_fence_after();
+      if (a.splits == 1) {
+        // O / l -> bf16, staged in Q_u (every S_u MMA completed before the last PV_u), stored coalesced
+        const float inv = l > 0.0f ? kUnshift * pair_factor<KV>() / l : 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          tcx::tmem_ld32(tO + 32u * c, o);
+          tcx::tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(sQ + tile_off(r, 4 * c + k)) =
+                make_uint4(pack_bf16(__uint_as_float(o[8 * k]) * inv, __uint_as_float(o[8 * k + 1]) * inv),
+                           pack_bf16(__uint_as_float(o[8 * k + 2]) * inv, __uint_as_float(o[8 * k + 3]) * inv),
+                           pack_bf16(__uint_as_float(o[8 * k + 4]) * inv, __uint_as_float(o[8 * k + 5]) * inv),
+                           pack_bf16(__uint_as_float(o[8 * k + 6]) * inv, __uint_as_float(o[8 * k + 7]) * inv));
+        }
+        tcx::tc_fence_before();
+        named_sync(1 + u, BM);
+        const int cc = r & 15;
+#pragma unroll 4
+        for (int it = 0; it < BM / 8; ++it) {
+          const int rr = it * 8 + (r >> 4);
+          if (Ru + rr < rw.n)
+            *reinterpret_cast<uint4*>(a.out + rw.id(a, Ru + rr, g) * HD + 8 * cc) =
+                *reinterpret_cast<const uint4*>(sQ + tile_off(rr, cc));
+        }
+      } else {
+        const int64_t at = split * n_rows_all + id;
+        const float fac = kUnshift * pair_factor<KV>();
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          tcx::tmem_ld32(tO + 32u * c, o);
+          tcx::tmem_ld_wait();
+          if (valid)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<float4*>(a.ws_o + at * HD + 32 * c + 4 * k) =
+                  make_float4(__uint_as_float(o[4 * k]) * fac, __uint_as_float(o[4 * k + 1]) * fac,
+                              __uint_as_float(o[4 * k + 2]) * fac, __uint_as_float(o[4 * k + 3]) * fac);
+        }
+        if (valid) {
+          a.ws_ml[2 * at] = m;
+          a.ws_ml[2 * at + 1] = l;
+        }
+        tcx::tc_fence_before();
+      }
+    }
+  }
+  tcx::tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tcx::tc_fence_after();
+    tcx::tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// Adds the splits' parts in order: one warp per packed row, lane owns dims 4 lane .. + 3.
+__global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs a) {
+  pdl_wait();      // inputs of this kernel are complete and visible
+  pdl_trigger();   // only now may the next kernel start its prologue
+  const int lane = threadIdx.x & 31, R = int(blockIdx.x) * 8 + int(threadIdx.x >> 5), g = blockIdx.y;
+  const Rows rw = rows_of(a, blockIdx.z);
+  if (R >= rw.n) return;
+  const int64_t id = rw.id(a, R, g), n = a.total_q * a.nh;
+  const float2* ml = reinterpret_cast<const float2*>(a.ws_ml);
+  float2 mine = make_float2(-INFINITY, 0.0f);   // part `lane` (at most 32)
+  if (lane < a.splits) mine = ml[lane * n + id];
+  const float M = warp_max(mine.x);
+  const float w = mine.x == -INFINITY ? 0.0f : ex2(mine.x - M);
+  const float l = warp_sum(mine.y * w);
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int i = 0; i < a.splits; ++i) {
+    const float wi = __shfl_sync(0xffffffffu, w, i);
+    if (wi == 0.0f) continue;   // (an empty part has no O)
+    const float4 x = *(reinterpret_cast<const float4*>(a.ws_o + (i * n + id) * HD) + lane);
+    acc.x = fmaf(x.x, wi, acc.x);
+    acc.y = fmaf(x.y, wi, acc.y);
+    acc.z = fmaf(x.z, wi, acc.z);
+    acc.w = fmaf(x.w, wi, acc.w);
+  }
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  *reinterpret_cast<uint2*>(a.out + id * HD + 4 * lane) =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+}
+
+// Shares that the key tiles are cut into: as many as still fit the GPU's SMs at
+// once, with four tiles each at least.  (Rows that fill the SMs by themselves are
+// not split.)
+int prefill_splits(int n_seqs, int max_q, int max_ctx, int nh, int nkv) {
+  constexpr int kSms = 152;
+  const int64_t ctas = (int64_t(max_q) * (nh / nkv) + ROWS - 1) / ROWS * nkv * n_seqs;
+  const int64_t tiles = (int64_t(max_ctx) + BN - 1) / BN;
+  return int(std::max<int64_t>(1, std::min({kSms / std::max<int64_t>(ctas, 1), tiles / 4, int64_t(32)})));
+}
+
+template <int KV>
+int launch(const PrefillArgs& a, int n_seqs, cudaStream_t st) {
+  static bool configured = false;
+  if (!configured) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(attn_prefill_kv8_kernel<KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(SMEM));
+    if (e != cudaSuccess) return set_error(QW_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    configured = true;
+  }
+  const int64_t rows = int64_t(a.max_q) * a.G;
+  const dim3 grid(unsigned((rows + ROWS - 1) / ROWS * a.splits), unsigned(a.nkv), unsigned(n_seqs));
+  launch_pdl(attn_prefill_kv8_kernel<KV>, grid, THREADS, SMEM, st, a);
+  int rc = check_launch("attn_prefill_kv8_kernel");
+  if (rc || a.splits == 1) return rc;
+  launch_pdl(prefill_merge_kernel, dim3(unsigned((rows + 7) / 8), unsigned(a.nkv), unsigned(n_seqs)), 256, 0, st, a);
+  return check_launch("prefill_merge_kernel");
+}
+
+}  // namespace kv8p
+
+namespace kv8 {
+int check_attention(const char* who, const void* k, const void* v, const float* ks, const float* vs, int64_t num_slots,
+                    int scale_block, const int32_t* table, int max_blocks, int block_size, int n_seqs, int max_context,
+                    int nh, int nkv, int head_dim, int window, int n_sink, int dtype, int kv_dtype);
+}
+
+unsigned int take_kv8_prefill_errors() {
+  unsigned int v = 0, z = 0;
+  cudaMemcpyFromSymbol(&v, kv8p::g_kv8_prefill_error, sizeof(v));
+  if (v) cudaMemcpyToSymbol(kv8p::g_kv8_prefill_error, &z, sizeof(z));
+  return v;
+}
+}  // namespace qw
+
+using namespace qw;
+
+extern "C" size_t qw_attention_prefill_kv8_workspace_size(int n_seqs, int64_t total_q, int max_seqlen_q,
+                                                          int max_context, int n_heads, int n_kv_heads) {
+  if (n_seqs <= 0 || total_q <= 0 || max_seqlen_q <= 0 || max_context < 0 || n_heads <= 0 || n_kv_heads <= 0) return 0;
+  const int s = kv8p::prefill_splits(n_seqs, max_seqlen_q, max_context, n_heads, n_kv_heads);
+  return s == 1 ? 0 : size_t(s) * size_t(total_q) * n_heads * (kv8::HD + 2) * sizeof(float);
+}
+
+extern "C" int qw_attention_prefill_kv8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                        const float* v_scale, int64_t num_slots, int scale_block,
+                                        const int32_t* cu_seqlens_q, const int32_t* context_lens,
+                                        const int32_t* block_table, int max_blocks, int block_size, int n_seqs,
+                                        int64_t total_q, int max_seqlen_q, int max_context, int n_heads,
+                                        int n_kv_heads, int head_dim, float scale, int window, int n_sink, void* out,
+                                        void* workspace, size_t workspace_bytes, int dtype, int kv_dtype,
+                                        void* stream) {
+  const char* who = "qw_attention_prefill_kv8";
+  if (total_q < 0 || max_seqlen_q < 0) return set_error(QW_ERR_INVALID_ARG, "%s: bad sizes", who);
+  const int rc = kv8::check_attention(who, k_cache, v_cache, k_scale, v_scale, num_slots, scale_block, block_table,
+                                      max_blocks, block_size, n_seqs, max_context, n_heads, n_kv_heads, head_dim,
+                                      window, n_sink, dtype, kv_dtype);
+  if (rc) return rc;
+  if (n_seqs > 65535 || n_kv_heads > 65535 || int64_t(max_seqlen_q) * (n_heads / n_kv_heads) > INT32_MAX)
+    return set_error(QW_ERR_SHAPE, "%s: more than 65535 sequences or kv heads, or 2^31 rows of a sequence", who);
+  if (n_seqs == 0 || max_seqlen_q == 0 || total_q == 0) return QW_OK;
+  if (!q || !cu_seqlens_q || !context_lens || !out) return set_error(QW_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!kv8::aligned16(q) || !kv8::aligned16(out))
+    return set_error(QW_ERR_INVALID_ARG, "%s: q and out must be 16-byte aligned", who);
+  const size_t need =
+      qw_attention_prefill_kv8_workspace_size(n_seqs, total_q, max_seqlen_q, max_context, n_heads, n_kv_heads);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return set_error(QW_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", who, need);
+  if (need > 0 && !kv8::aligned16(workspace))
+    return set_error(QW_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", who);
+  kv8p::PrefillArgs a;
+  a.q = static_cast<const bf16*>(q);
+  a.c = kv8::Cache{k_cache, v_cache, k_scale, v_scale, num_slots, kv8::scale_shift(scale_block), block_table, max_blocks,
+                   block_size};
+  a.cu_q = cu_seqlens_q;
+  a.ctx = context_lens;
+  a.total_q = total_q;
+  a.max_q = max_seqlen_q;
+  a.max_ctx = max_context;
+  a.nh = n_heads;
+  a.nkv = n_kv_heads;
+  a.G = n_heads / n_kv_heads;
+  a.window = window;
+  a.n_sink = n_sink;
+  a.splits = kv8p::prefill_splits(n_seqs, max_seqlen_q, max_context, n_heads, n_kv_heads);
+  a.scale_log2 = fabsf(scale) * kv8p::kLog2e;
+  a.q_sign = scale < 0.0f ? -1.0f : 1.0f;
+  a.out = static_cast<bf16*>(out);
+  a.ws_o = static_cast<float*>(workspace);
+  a.ws_ml = need > 0 ? a.ws_o + size_t(a.splits) * size_t(total_q) * n_heads * kv8::HD : nullptr;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return kv_dtype == QW_I8 ? kv8p::launch<QW_I8>(a, n_seqs, st) : kv8p::launch<QW_E4M3>(a, n_seqs, st);
+}
