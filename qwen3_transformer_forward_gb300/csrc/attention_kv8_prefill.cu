@@ -57,6 +57,7 @@ constexpr float kRescaleLog2 = 8.0f, kShift = 7.0f, kUnshift = 1.0f / 128.0f;
 // Past this |m| the exponent is formed as (x - m) + 7 instead of one fused step,
 // whose constant log2(v_scale) - m + 7 would be rounded too coarsely.
 constexpr float kBigScore = 512.0f;
+constexpr float kTinyFactor = 1e-30f;   // score factors are never zero, so that a masked -inf stays one
 
 constexpr int B_K_FULL = 0, B_K_EMPTY = 2, B_V_FULL = 4, B_V_EMPTY = 6, B_Q = 8, B_S_FULL = 10, B_P_FULL = 12,
               B_O_DONE = 14, B_DONE = 16, N_BARS = 17;
@@ -71,24 +72,62 @@ __device__ __forceinline__ uint32_t tile_off(int r, int c) {   // row r, 16-byte
   return uint32_t(c >> 3) * BOX + uint32_t(r) * 128u + (uint32_t((c & 7) ^ (r & 7)) << 4);
 }
 __device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// One MMA step, issued by the lane with `lead`.  Descriptors come as their low
+// words (the start address moves, the rest is one constant for each layout), and
+// the lead is a predicate, not a branch: the issuing warp stays convergent and its
+// operands in uniform registers.  (Building each 64-bit descriptor inside an
+// `if (lane == 0)` took the issuing thread 5600 cycles a key tile, against 2050 of
+// tensor pipe work.)
+__device__ __forceinline__ void umma_ss(uint32_t lead, uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
+                                        uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n .reg .pred p, q;\n .reg .b64 x, y;\n setp.ne.b32 q, %0, 0;\n setp.ne.b32 p, %6, 0;\n"
+      " mov.b64 x, {%2, %4};\n mov.b64 y, {%3, %4};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%1], x, y, %5, p;\n}\n" ::"r"(lead),
+      "r"(d), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void umma_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi,
+                                        uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n .reg .pred p, q;\n .reg .b64 y;\n setp.ne.b32 q, %0, 0;\n setp.ne.b32 p, %6, 0;\n"
+      " mov.b64 y, {%3, %4};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], y, %5, p;\n}\n" ::"r"(lead),
+      "r"(d), "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc)
       : "memory");
 }
-template <int N> __device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> __device__ __forceinline__ void regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-// Registers at launch: 128 a thread.  4 warpgroups: 40 + 104 + 184 + 184 = 4 * 128.
-constexpr int kRegsIssue = 40, kRegsConvert = 104, kRegsSoftmax = 184;
-static_assert(kRegsIssue + kRegsConvert + 2 * kRegsSoftmax <= 4 * 128, "register pool of one CTA");
-
+__device__ __forceinline__ void commit(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %0, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n}\n" ::"r"(lead),
+      "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r;
+}
+// 64 columns of TMEM, arrived (load and wait in one statement: no use can come between)
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63"
+      "}, [%64];\n tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ uint64_t pair64(float a, float b) {
   uint64_t d;
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
@@ -226,28 +265,28 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
   };
 
   if (warp < 4) {
-    regs_less<kRegsIssue>();
-    // ---------------- MMA issuer (one thread) ----------------
-    if (warp == 0 && lane == 0) {
+    // ---------------- MMA issuer (warp 0, one elected lane) ----------------
+    if (warp == 0) {
+      const uint32_t lead = elect_one();
+      const uint64_t dk = tcx::sw128_desc(sbase), dv = tcx::sw128_desc_mn(sbase, BOX);   // + (offset >> 4)
+      const uint32_t k_lo = uint32_t(dk), k_hi = uint32_t(dk >> 32), v_lo = uint32_t(dv), v_hi = uint32_t(dv >> 32);
       auto issue_s = [&](int u, int j) {   // S_u(j) = Q_u K_j^T
-        const uint32_t qaddr = sbase + OFF_Q + uint32_t(u) * TILE;
-        const uint32_t kaddr = sbase + OFF_K + uint32_t(j & 1) * TILE;
+        const uint32_t qd = k_lo + ((OFF_Q + uint32_t(u) * TILE) >> 4), kd = k_lo + ((OFF_K + uint32_t(j & 1) * TILE) >> 4);
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk) {
-          const uint32_t off = uint32_t(kk >> 2) * BOX + uint32_t(kk & 3) * 32u;
-          umma_ss(tmem + uint32_t(u) * 128u, tcx::sw128_desc(qaddr + off), tcx::sw128_desc(kaddr + off), IDESC_S,
-                  kk > 0 ? 1u : 0u);
+          const uint32_t off = (uint32_t(kk >> 2) * BOX + uint32_t(kk & 3) * 32u) >> 4;
+          umma_ss(lead, tmem + uint32_t(u) * 128u, qd + off, kd + off, k_hi, IDESC_S, kk > 0 ? 1u : 0u);
         }
-        tcx::umma_commit(bar(B_S_FULL + u));
+        commit(lead, bar(B_S_FULL + u));
       };
       auto issue_pv = [&](int u, int j) {   // O_u += P_u V_j
-        const uint32_t vaddr = sbase + OFF_V + uint32_t(j & 1) * TILE;
+        const uint32_t vd = v_lo + ((OFF_V + uint32_t(j & 1) * TILE) >> 4);
         const uint32_t tS = tmem + uint32_t(u) * 128u;
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk)
-          umma_ts(tS + 256u, tS + uint32_t(kk) * 8u, tcx::sw128_desc_mn(vaddr + uint32_t(kk) * 2048u, BOX), IDESC_PV,
+          umma_ts(lead, tS + 256u, tS + uint32_t(kk) * 8u, vd + uint32_t(kk) * (2048u >> 4), v_hi, IDESC_PV,
                   (j > 0 || kk > 0) ? 1u : 0u);
-        tcx::umma_commit(bar(B_O_DONE + u));
+        commit(lead, bar(B_O_DONE + u));
       };
       if (n_u[0] > 0) wait(B_Q, 0u, 5u);
       if (n_u[1] > 0) wait(B_Q + 1, 0u, 5u);
@@ -255,7 +294,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
       tcx::tc_fence_after();
       if (n_u[0] > 0) issue_s(0, 0);
       if (n_u[1] > 0) issue_s(1, 0);
-      tcx::umma_commit(bar(B_K_EMPTY));   // K_0 released once both S(0) complete
+      commit(lead, bar(B_K_EMPTY));   // K_0 released once both S(0) complete
       for (int j = 0; j < n_kv; ++j) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -272,16 +311,15 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
             }
           }
         }
-        tcx::umma_commit(bar(B_V_EMPTY + (j & 1)));
-        if (j + 1 < n_kv) tcx::umma_commit(bar(B_K_EMPTY + ((j + 1) & 1)));
+        commit(lead, bar(B_V_EMPTY + (j & 1)));
+        if (j + 1 < n_kv) commit(lead, bar(B_K_EMPTY + ((j + 1) & 1)));
       }
       // every MMA of this CTA has completed before TMEM is released
-      tcx::umma_commit(bar(B_DONE));
+      commit(lead, bar(B_DONE));
       wait(B_DONE, 0u, 11u);
     }
     __syncwarp();
   } else if (warp < 8) {
-    regs_less<kRegsConvert>();
     // ---------------- converters: warp w holds keys 32 w .. + 31 of every tile ----------------
     const int w = warp - 4, rsub = lane >> 2, c4 = lane & 3;
     const int64_t row_bytes = int64_t(a.nkv) * HD;
@@ -374,7 +412,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
       if (j + 1 < n_kv) load(vr, a.c.v);
     }
   } else {
-    regs_more<kRegsSoftmax>();
     // ---------------- softmax (one query row per thread) ----------------
     const int u = (warp - 8) >> 2;
     const int quarter = warp & 3;             // TMEM lanes this warp may access
@@ -424,39 +461,36 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
         // S_u(j) complete, and with it every earlier MMA (O_u holds PV_u(j-1))
         wait(B_S_FULL + u, uint32_t(j) & 1u, 12u);
         tcx::tc_fence_after();
-        uint32_t sr[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tcx::tmem_ld32(tS + 32u * c, sr[c]);
-        tcx::tmem_ld_wait();
         const int k0 = tile_key(j);
-        const bool whole = k0 + BN <= hi && (k0 >= lo_row || k0 + BN <= a.n_sink);
-        if (!whole) {
-          const int end = hi - k0, beg = lo_row - k0, snk = a.n_sink - k0;   // columns [beg, end) and [0, min(snk, end))
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int col = 32 * c + e;
-              if (!(col < end && (col >= beg || col < snk))) sr[c][e] = __float_as_uint(-INFINITY);
-            }
-        }
+        const int end = hi - k0, beg = lo_row - k0, snk = a.n_sink - k0;   // columns [beg, end) and [0, min(snk, end))
         const float4* scl = reinterpret_cast<const float4*>(sm + OFF_SCL) + (j & 3) * 8;
-        float fb[8], lb[8], m_tile = -INFINITY;
+        // Two passes over S in halves of 64 columns: the maximum, then the weights.  (S held in
+        // 128 registers and the loops unrolled over all of it ran out of the instruction
+        // cache: 4000 cycles a tile.)
+        uint32_t x[64];
+        auto load = [&](int c) {
+          tmem_ld64(tS + 64u * c, x);
+          const int c0 = 64 * c;
+          if (!(c0 + 64 <= end && (c0 >= beg || c0 + 64 <= snk)))
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
-          const uint32_t* x = &sr[b >> 1][16 * (b & 1)];
-          float mx0 = __uint_as_float(x[0]), mx1 = __uint_as_float(x[1]);
+            for (int e = 0; e < 64; ++e)
+              if (!(c0 + e < end && (c0 + e >= beg || c0 + e < snk))) x[e] = __float_as_uint(-INFINITY);
+        };
+        float m_tile = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          load(c);
 #pragma unroll
-          for (int e = 2; e < 16; e += 2) {
-            mx0 = fmaxf(mx0, __uint_as_float(x[e]));
-            mx1 = fmaxf(mx1, __uint_as_float(x[e + 1]));
+          for (int b = 0; b < 4; ++b) {
+            float mx[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(x[16 * b + e]);
+#pragma unroll
+            for (int e = 4; e < 16; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(x[16 * b + e]));
+            const float4 sc = scl[4 * c + b];
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            m_tile = fmaxf(m_tile, fmaf(top, fmaxf(rowf * sc.x, kTinyFactor), sc.y));
           }
-          const float mx = fmaxf(mx0, mx1);
-          const float4 sc = scl[b];
-          fb[b] = rowf * sc.x;
-          lb[b] = sc.y;
-          // (a block without a visible key: -inf, whatever the factor)
-          m_tile = fmaxf(m_tile, mx == -INFINITY ? -INFINITY : fmaf(mx, fb[b], lb[b]));
         }
         float alpha = 1.0f;
         bool rescale = false;
@@ -468,34 +502,37 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
         const float m_use = m == -INFINITY ? 0.0f : m;
         l *= alpha;
         const bool big = __any_sync(0xffffffffu, fabsf(m_use) > kBigScore);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 2; ++c) {
+          load(c);
           uint32_t pk[32];
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const int b = 4 * c + h;
-            uint32_t* x = &sr[b >> 1][16 * (b & 1)];
-            uint64_t sum = 0;
-            const float cb = lb[b] - m_use + kShift;
-            const uint64_t f2 = pair64(fb[b], fb[b]), c2 = pair64(cb, cb);
+          for (int b = 0; b < 4; ++b) {
+            const float4 sc = scl[4 * c + b];
+            float f = fmaxf(rowf * sc.x, kTinyFactor), cb = sc.y - m_use + kShift;
+            if (big) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                x[16 * b + e] = __float_as_uint(fmaf(__uint_as_float(x[16 * b + e]), f, sc.y) - m_use + kShift);
+              f = 1.0f;
+              cb = 0.0f;
+            }
+            const uint64_t f2 = pair64(f, f), c2 = pair64(cb, cb);
+            uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
-              float x0 = __uint_as_float(x[e]), x1 = __uint_as_float(x[e + 1]);
-              if (big || !whole) {   // (a factor of zero times -inf is NaN: masked columns stay -inf)
-                x0 = x0 == -INFINITY ? x0 : fmaf(x0, fb[b], lb[b]) - m_use + kShift;
-                x1 = x1 == -INFINITY ? x1 : fmaf(x1, fb[b], lb[b]) - m_use + kShift;
-              } else {
-                unpair64(fma2(pair64(x0, x1), f2, c2), x0, x1);
-              }
-              const float p0 = ex2(x0), p1 = ex2(x1);
+              float y0, y1;
+              unpair64(fma2(pair64(__uint_as_float(x[16 * b + e]), __uint_as_float(x[16 * b + e + 1])), f2, c2), y0, y1);
+              const float p0 = ex2(y0), p1 = ex2(y1);
+              uint64_t& sum = e & 2 ? sum1 : sum0;
               sum = add2(sum, pair64(p0, p1));
-              pk[8 * h + e / 2] = pack_f16(p0, p1);
+              pk[8 * b + e / 2] = pack_f16(p0, p1);
             }
             float s0, s1;
-            unpair64(sum, s0, s1);
-            l = fmaf(s0 + s1, scl[b].z, l);
+            unpair64(add2(sum0, sum1), s0, s1);
+            l = fmaf(s0 + s1, sc.z, l);
           }
-          tcx::tmem_st32(tS + 32u * c, pk);   // P_u(j): keys 64 c .. + 63
+          tcx::tmem_st32(tS + 32u * c, pk);   // P_u(j), keys 64 c .. + 63: over columns of S that were read
         }
         if (j >= 1 && __any_sync(0xffffffffu, rescale)) {
 #pragma unroll 1
