@@ -42,7 +42,7 @@ using namespace kv8;
 
 __device__ unsigned int g_kv8_prefill_error = 0;
 
-constexpr int BM = 128, BN = 128, ROWS = 2 * BM, THREADS = 512;
+constexpr int BM = 128, BN = 128, HALF = 64, ROWS = 2 * BM, THREADS = 512;
 constexpr uint32_t BOX = 16384;                    // 128 rows x 64 f16
 constexpr uint32_t TILE = 2 * BOX;                 // 128 rows x 128 f16
 constexpr uint32_t OFF_Q = 0;                      // Q_0, Q_1 (then the output staging)
@@ -59,13 +59,16 @@ constexpr float kRescaleLog2 = 8.0f, kShift = 7.0f, kUnshift = 1.0f / 128.0f;
 constexpr float kBigScore = 512.0f;
 constexpr float kTinyFactor = 1e-30f;   // score factors are never zero, so that a masked -inf stays one
 
-constexpr int B_K_FULL = 0, B_K_EMPTY = 2, B_V_FULL = 4, B_V_EMPTY = 6, B_Q = 8, B_S_FULL = 10, B_P_FULL = 12,
-              B_O_DONE = 14, B_DONE = 16, N_BARS = 17;
+// B_S_FULL and B_P_FULL + 2 u + buffer.  (P needs one for each buffer: a softmax warp may
+// finish step t + 1 before the MMA warp has seen step t.  The last PV has one of its own:
+// after P(last) up to two phases of B_O_DONE are open, which a parity cannot tell apart.)
+constexpr int B_K_FULL = 0, B_K_EMPTY = 2, B_V_FULL = 4, B_V_EMPTY = 6, B_Q = 8, B_S_FULL = 10, B_P_FULL = 14,
+              B_O_DONE = 18, B_O_LAST = 20, B_DONE = 22, N_BARS = 23;
 static_assert(N_BARS * 8 + 4 <= 256, "barrier area");
 
 // kind::f16 instruction descriptor with f16 A and B, fp32 D
 constexpr uint32_t idesc_f16(int M, int N) { return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24); }
-constexpr uint32_t IDESC_S = idesc_f16(BM, BN);
+constexpr uint32_t IDESC_S = idesc_f16(BM, HALF);
 constexpr uint32_t IDESC_PV = idesc_f16(BM, HD) | tcx::kIdescBMajorMN;
 
 __device__ __forceinline__ uint32_t tile_off(int r, int c) {   // row r, 16-byte chunk c of 16
@@ -163,7 +166,8 @@ struct PrefillArgs {
 struct Rows {
   int qs, lq, start, n;   // first token, new tokens, key position of token 0, packed rows that exist
   __device__ __forceinline__ int64_t id(const PrefillArgs& a, int R, int g) const {   // row of q and out
-    return (int64_t(qs) + R / a.G) * a.nh + g * a.G + R % a.G;
+    const int tok = R / a.G;
+    return (int64_t(qs) + tok) * a.nh + g * a.G + (R - tok * a.G);
   }
 };
 __device__ __forceinline__ Rows rows_of(const PrefillArgs& a, int s) {
@@ -201,12 +205,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
   const int lo_cta = a.window > 0 ? max(p_lo + 1 - a.window, 0) : 0;
   const int w0 = lo_cta / BN;
   const int ns = min((min(a.n_sink, lo_cta) + BN - 1) / BN, w0);
-  int n_u[2], hi_cta = 0;
+  int n_u[2], hi_u[2], hi_cta = 0;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int last = min(R0 + BM * u + BM, rw.n) - 1;             // the unit's last row
     const int hi = last >= R0 + BM * u ? min(rw.start + last / a.G + 1, cap) : 0;   // keys its rows see end here
     hi_cta = max(hi_cta, hi);
+    hi_u[u] = hi;
     const int tb = hi > 0 ? (hi + BN - 1) / BN : 0;
     n_u[u] = tb > w0 ? ns + tb - w0 : min(ns, tb);
   }
@@ -214,8 +219,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
   const int t0 = int(int64_t(n_all) * split / a.splits), t1 = int(int64_t(n_all) * (split + 1) / a.splits);
 #pragma unroll
   for (int u = 0; u < 2; ++u) n_u[u] = max(min(n_u[u], t1) - t0, 0);
-  const int n_kv = max(n_u[0], n_u[1]);
+  const int n_kv = max(n_u[0], n_u[1]);                           // tiles of this CTA
   auto tile_key = [&](int j) { return (t0 + j < ns ? t0 + j : w0 + t0 + j - ns) * BN; };   // first key of tile j
+  int s_u[2];   // steps of 64 keys: two a tile, without a last one that the unit does not see
+#pragma unroll
+  for (int u = 0; u < 2; ++u) s_u[u] = 2 * n_u[u] - (n_u[u] > 0 && tile_key(n_u[u] - 1) + HALF >= hi_u[u] ? 1 : 0);
   const int64_t n_rows_all = a.total_q * a.nh;
 
   // rows without a tile: zero output, or an empty part
@@ -245,8 +253,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
       tcx::mbar_init(bar(B_V_EMPTY + i), 1);
       tcx::mbar_init(bar(B_Q + i), BM);
       tcx::mbar_init(bar(B_S_FULL + i), 1);
+      tcx::mbar_init(bar(B_S_FULL + 2 + i), 1);
       tcx::mbar_init(bar(B_P_FULL + i), 4);
+      tcx::mbar_init(bar(B_P_FULL + 2 + i), 4);
       tcx::mbar_init(bar(B_O_DONE + i), 1);
+      tcx::mbar_init(bar(B_O_LAST + i), 1);
     }
     tcx::mbar_init(bar(B_DONE), 1);
     tcx::fence_mbar_init();
@@ -254,6 +265,77 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
   if (warp == 0) {
     tcx::tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
     tcx::tmem_relinquish();
+  }
+  // ---- every role's first reads, before the barrier that the set-up ends with
+  // converters: warp w holds keys 32 w .. + 31 of every tile
+  const int w = warp - 4, rsub = lane >> 2, c4 = lane & 3;
+  const int64_t row_bytes = int64_t(a.nkv) * HD;
+  uint4 kr[8], vr[8];
+  float sk = 0.0f, sv = 0.0f;            // lanes 0, 1: scales of the warp's two blocks
+  int64_t row0 = -1;                     // cache row of the warp's first key
+  bool has[2] = {false, false};          // its two blocks are seen by some row and have a page
+  auto find = [&](int j) {
+    const int key0 = tile_key(j) + 32 * w;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int k = key0 + 16 * b;
+      has[b] = max(k, lo_cta) < min(k + 16, hi_cta) || k < min(a.n_sink, hi_cta);
+    }
+    row0 = has[0] || has[1] ? row_of(a.c.table, a.c.max_blocks, a.c.block_size, a.c.num_slots, s, key0) : -1;
+    if (row0 < 0) has[0] = has[1] = false;
+    if (row0 + 16 >= a.c.num_slots) has[1] = false;   // (the cache may end inside a page, after a whole block)
+  };
+  auto load = [&](uint4 (&x)[8], const void* cache) {
+    const uint8_t* base = static_cast<const uint8_t*>(cache) + (row0 + rsub) * row_bytes + int64_t(g) * HD + 16 * c4;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        x[2 * k + b] = has[k >> 1] ? __ldg(reinterpret_cast<const uint4*>(base + 8 * k * row_bytes + 64 * b))
+                                   : make_uint4(0u, 0u, 0u, 0u);
+  };
+  auto load_scales = [&]() {
+    sk = sv = 0.0f;
+    if (lane < 2 && (lane ? has[1] : has[0])) {
+      const int64_t at = ((row0 + 16 * lane) >> a.c.sb_shift) * a.nkv + g;
+      sk = a.c.k_scale[at];
+      sv = a.c.v_scale[at];
+    }
+  };
+  // softmax warps: one query row per thread, TMEM lane = row
+  const int u = (warp >> 2) & 1, quarter = warp & 3, r = quarter * 32 + lane;
+  const int Ru = R0 + BM * u;
+  uint8_t* sQ = sm + OFF_Q + u * TILE;
+  const bool valid = Ru + r < rw.n;
+  const int64_t id = rw.id(a, valid ? Ru + r : Ru, g);
+  float rowf = 0.0f;
+  if (warp >= 8) {
+    uint4 x[16];
+    float top = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+      x[c] = valid ? *reinterpret_cast<const uint4*>(a.q + id * HD + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const uint32_t wd[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(wd[e])), fabsf(bf16_hi(wd[e]))));
+    }
+    float mul, inv;
+    row_scale(top, mul, inv);
+    mul *= a.q_sign;
+    rowf = inv * a.scale_log2 * pair_factor<KV>();
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      auto cv = [&](uint32_t v) { return pack_f16(bf16_lo(v) * mul, bf16_hi(v) * mul); };
+      *reinterpret_cast<uint4*>(sQ + tile_off(r, c)) = make_uint4(cv(x[c].x), cv(x[c].y), cv(x[c].z), cv(x[c].w));
+    }
+    tcx::fence_proxy_async();
+  } else if (warp >= 4) {
+    find(0);
+    load_scales();
+    load(kr, a.c.k);
+    load(vr, a.c.v);
   }
   tcx::tc_fence_before();
   __syncthreads();
@@ -270,49 +352,58 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
       const uint32_t lead = elect_one();
       const uint64_t dk = tcx::sw128_desc(sbase), dv = tcx::sw128_desc_mn(sbase, BOX);   // + (offset >> 4)
       const uint32_t k_lo = uint32_t(dk), k_hi = uint32_t(dk >> 32), v_lo = uint32_t(dv), v_hi = uint32_t(dv >> 32);
-      auto issue_s = [&](int u, int j) {   // S_u(j) = Q_u K_j^T
-        const uint32_t qd = k_lo + ((OFF_Q + uint32_t(u) * TILE) >> 4), kd = k_lo + ((OFF_K + uint32_t(j & 1) * TILE) >> 4);
+      auto issue_s = [&](int u, int t) {   // S_u(t) = Q_u K^T: keys 64 (t & 1) .. + 63 of tile t / 2
+        const uint32_t qd = k_lo + ((OFF_Q + uint32_t(u) * TILE) >> 4);
+        const uint32_t kd = k_lo + ((OFF_K + uint32_t((t >> 1) & 1) * TILE + uint32_t(t & 1) * (BOX / 2)) >> 4);
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk) {
           const uint32_t off = (uint32_t(kk >> 2) * BOX + uint32_t(kk & 3) * 32u) >> 4;
-          umma_ss(lead, tmem + uint32_t(u) * 128u, qd + off, kd + off, k_hi, IDESC_S, kk > 0 ? 1u : 0u);
+          umma_ss(lead, tmem + uint32_t(u) * 128u + uint32_t(t & 1) * 64u, qd + off, kd + off, k_hi, IDESC_S,
+                  kk > 0 ? 1u : 0u);
         }
-        commit(lead, bar(B_S_FULL + u));
+        commit(lead, bar(B_S_FULL + 2 * u + (t & 1)));
       };
-      auto issue_pv = [&](int u, int j) {   // O_u += P_u V_j
-        const uint32_t vd = v_lo + ((OFF_V + uint32_t(j & 1) * TILE) >> 4);
-        const uint32_t tS = tmem + uint32_t(u) * 128u;
+      auto issue_pv = [&](int u, int t) {   // O_u += P_u(t) V
+        const uint32_t vd = v_lo + ((OFF_V + uint32_t((t >> 1) & 1) * TILE + uint32_t(t & 1) * (BOX / 2)) >> 4);
+        const uint32_t tP = tmem + uint32_t(u) * 128u + uint32_t(t & 1) * 64u;
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
-          umma_ts(lead, tS + 256u, tS + uint32_t(kk) * 8u, vd + uint32_t(kk) * (2048u >> 4), v_hi, IDESC_PV,
-                  (j > 0 || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < HALF / 16; ++kk)
+          umma_ts(lead, tmem + 256u + uint32_t(u) * 128u, tP + uint32_t(kk) * 8u, vd + uint32_t(kk) * (2048u >> 4), v_hi,
+                  IDESC_PV, (t > 0 || kk > 0) ? 1u : 0u);
         commit(lead, bar(B_O_DONE + u));
+        if (t + 1 == s_u[u]) commit(lead, bar(B_O_LAST + u));
       };
-      if (n_u[0] > 0) wait(B_Q, 0u, 5u);
-      if (n_u[1] > 0) wait(B_Q + 1, 0u, 5u);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (s_u[u] > 0) wait(B_Q + u, 0u, 5u);
       wait(B_K_FULL, 0u, 6u);
       tcx::tc_fence_after();
-      if (n_u[0] > 0) issue_s(0, 0);
-      if (n_u[1] > 0) issue_s(1, 0);
-      commit(lead, bar(B_K_EMPTY));   // K_0 released once both S(0) complete
-      for (int j = 0; j < n_kv; ++j) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (j < n_u[u]) {
-            // P_u(j) written; its softmax also saw V_j (and K_{j+1}) land
-            wait(B_P_FULL + u, uint32_t(j) & 1u, 8u);
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (t < s_u[u]) issue_s(u, t);
+      commit(lead, bar(B_K_EMPTY));   // K_0 is free once these complete
+      const int steps = max(s_u[0], s_u[1]);
+      for (int t = 0; t < steps; ++t) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (t < s_u[u]) {
+            // P_u(t) written; its softmax also saw V of this tile (and, t even, K of the next) land
+            wait(B_P_FULL + 2 * u + (t & 1), uint32_t(t >> 1) & 1u, 8u);
             tcx::tc_fence_after();
-            issue_pv(u, j);
-            if (j + 1 < n_u[u]) {
-              // S_u(j+1) overwrites the P_u(j) that PV_u(j) reads
-              wait(B_O_DONE + u, uint32_t(j) & 1u, 10u);
-              tcx::tc_fence_after();
-              issue_s(u, j + 1);
-            }
+            issue_pv(u, t);
           }
-        }
-        commit(lead, bar(B_V_EMPTY + (j & 1)));
-        if (j + 1 < n_kv) commit(lead, bar(B_K_EMPTY + ((j + 1) & 1)));
+        if (t & 1) commit(lead, bar(B_V_EMPTY + ((t >> 1) & 1)));
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (t + 2 < s_u[u]) {
+            // S_u(t+2) overwrites the P_u(t) that PV_u(t) reads
+            wait(B_O_DONE + u, uint32_t(t) & 1u, 10u);
+            tcx::tc_fence_after();
+            issue_s(u, t + 2);
+          }
+        if (t & 1) commit(lead, bar(B_K_EMPTY + (((t + 2) >> 1) & 1)));
       }
       // every MMA of this CTA has completed before TMEM is released
       commit(lead, bar(B_DONE));
@@ -321,40 +412,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
     __syncwarp();
   } else if (warp < 8) {
     // ---------------- converters: warp w holds keys 32 w .. + 31 of every tile ----------------
-    const int w = warp - 4, rsub = lane >> 2, c4 = lane & 3;
-    const int64_t row_bytes = int64_t(a.nkv) * HD;
-    uint4 kr[8], vr[8];
-    float sk = 0.0f, sv = 0.0f;            // lanes 0, 1: scales of the warp's two blocks
-    int64_t row0 = -1;                     // cache row of the warp's first key
-    bool has[2] = {false, false};          // its two blocks are seen by some row and have a page
-    auto find = [&](int j) {
-      const int key0 = tile_key(j) + 32 * w;
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int k = key0 + 16 * b;
-        has[b] = max(k, lo_cta) < min(k + 16, hi_cta) || k < min(a.n_sink, hi_cta);
-      }
-      row0 = has[0] || has[1] ? row_of(a.c.table, a.c.max_blocks, a.c.block_size, a.c.num_slots, s, key0) : -1;
-      if (row0 < 0) has[0] = has[1] = false;
-      if (row0 + 16 >= a.c.num_slots) has[1] = false;   // (the cache may end inside a page, after a whole block)
-    };
-    auto load = [&](uint4 (&x)[8], const void* cache) {
-      const uint8_t* base = static_cast<const uint8_t*>(cache) + (row0 + rsub) * row_bytes + int64_t(g) * HD + 16 * c4;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-          x[2 * k + b] = has[k >> 1] ? __ldg(reinterpret_cast<const uint4*>(base + 8 * k * row_bytes + 64 * b))
-                                     : make_uint4(0u, 0u, 0u, 0u);
-    };
-    auto load_scales = [&]() {
-      sk = sv = 0.0f;
-      if (lane < 2 && (lane ? has[1] : has[0])) {
-        const int64_t at = ((row0 + 16 * lane) >> a.c.sb_shift) * a.nkv + g;
-        sk = a.c.k_scale[at];
-        sv = a.c.v_scale[at];
-      }
-    };
     auto store = [&](const uint4 (&x)[8], uint32_t off) {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
@@ -376,10 +433,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
       __syncwarp();
       if (lane == 0) tcx::mbar_arrive(bar(b));
     };
-    find(0);
-    load_scales();
-    load(kr, a.c.k);
-    load(vr, a.c.v);
     for (int j = 0; j < n_kv; ++j) {
       const int slot = j & 1;
       bool zero_v[2];   // blocks whose v_scale counts as zero
@@ -413,42 +466,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
     }
   } else {
     // ---------------- softmax (one query row per thread) ----------------
-    const int u = (warp - 8) >> 2;
-    const int quarter = warp & 3;             // TMEM lanes this warp may access
-    const int r = quarter * 32 + lane;        // row within the unit
-    const int nu = u ? n_u[1] : n_u[0];
-    const int Ru = R0 + BM * u;
-    uint8_t* sQ = sm + OFF_Q + u * TILE;
-    if (nu == 0) {
+    const int steps = u ? s_u[1] : s_u[0];
+    if (steps == 0) {
       no_tiles(Ru, BM, r, BM);
     } else {
-      const bool valid = Ru + r < rw.n;
-      const int64_t id = rw.id(a, valid ? Ru + r : Ru, g);
-      float rowf;
-      {
-        uint4 x[16];
-        float top = 0.0f;
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          x[c] = valid ? *reinterpret_cast<const uint4*>(a.q + id * HD + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t wd[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(wd[e])), fabsf(bf16_hi(wd[e]))));
-        }
-        float mul, inv;
-        row_scale(top, mul, inv);
-        mul *= a.q_sign;
-        rowf = inv * a.scale_log2 * pair_factor<KV>();
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          auto cv = [&](uint32_t v) { return pack_f16(bf16_lo(v) * mul, bf16_hi(v) * mul); };
-          *reinterpret_cast<uint4*>(sQ + tile_off(r, c)) = make_uint4(cv(x[c].x), cv(x[c].y), cv(x[c].z), cv(x[c].w));
-        }
-      }
       // The first tile's scales.  Waited for before this thread lets S(0) start: the slot is
       // filled again only after S(0), so this phase cannot be missed.
       wait(B_K_FULL, 0u, 14u);
-      tcx::fence_proxy_async();
       tcx::mbar_arrive(bar(B_Q + u));
 
       const int p = rw.start + (Ru + r) / a.G;              // key position of this row
@@ -457,84 +481,74 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
       const uint32_t tS = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(u) * 128u;
       const uint32_t tO = tS + 256u;
       float m = -INFINITY, l = 0.0f;
-      for (int j = 0; j < nu; ++j) {
-        // S_u(j) complete, and with it every earlier MMA (O_u holds PV_u(j-1))
-        wait(B_S_FULL + u, uint32_t(j) & 1u, 12u);
+      for (int t = 0; t < steps; ++t) {
+        const int j = t >> 1;
+        const uint32_t tX = tS + uint32_t(t & 1) * 64u;   // S_u(t), then P_u(t) over its first 32 columns
+        wait(B_S_FULL + 2 * u + (t & 1), uint32_t(t >> 1) & 1u, 12u);
         tcx::tc_fence_after();
-        const int k0 = tile_key(j);
-        const int end = hi - k0, beg = lo_row - k0, snk = a.n_sink - k0;   // columns [beg, end) and [0, min(snk, end))
-        const float4* scl = reinterpret_cast<const float4*>(sm + OFF_SCL) + (j & 3) * 8;
-        // Two passes over S in halves of 64 columns: the maximum, then the weights.  (S held in
-        // 128 registers and the loops unrolled over all of it ran out of the instruction
-        // cache: 4000 cycles a tile.)
         uint32_t x[64];
-        auto load = [&](int c) {
-          tmem_ld64(tS + 64u * c, x);
-          const int c0 = 64 * c;
-          if (!(c0 + 64 <= end && (c0 >= beg || c0 + 64 <= snk)))
+        tmem_ld64(tX, x);
+        const int k0 = tile_key(j) + HALF * (t & 1);
+        const int end = hi - k0, beg = lo_row - k0, snk = a.n_sink - k0;   // columns [beg, end) and [0, min(snk, end))
+        if (!(HALF <= end && (0 >= beg || HALF <= snk)))
 #pragma unroll
-            for (int e = 0; e < 64; ++e)
-              if (!(c0 + e < end && (c0 + e >= beg || c0 + e < snk))) x[e] = __float_as_uint(-INFINITY);
-        };
-        float m_tile = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          load(c);
+          for (int e = 0; e < HALF; ++e)
+            if (!(e < end && (e >= beg || e < snk))) x[e] = __float_as_uint(-INFINITY);
+        const float4* scl = reinterpret_cast<const float4*>(sm + OFF_SCL) + (j & 3) * 8 + 4 * (t & 1);
+        float fb[4], m_step = -INFINITY;
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            float mx[4];
+        for (int b = 0; b < 4; ++b) {
+          float mx[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(x[16 * b + e]);
+          for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(x[16 * b + e]);
 #pragma unroll
-            for (int e = 4; e < 16; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(x[16 * b + e]));
-            const float4 sc = scl[4 * c + b];
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            m_tile = fmaxf(m_tile, fmaf(top, fmaxf(rowf * sc.x, kTinyFactor), sc.y));
-          }
+          for (int e = 4; e < 16; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(x[16 * b + e]));
+          const float4 sc = scl[b];
+          fb[b] = fmaxf(rowf * sc.x, kTinyFactor);
+          m_step = fmaxf(m_step, fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fb[b], sc.y));
         }
         float alpha = 1.0f;
         bool rescale = false;
-        if (m_tile > m + kRescaleLog2) {
-          alpha = ex2(m - m_tile);
-          m = m_tile;
+        if (m_step > m + kRescaleLog2) {
+          alpha = ex2(m - m_step);
+          m = m_step;
           rescale = true;
         }
         const float m_use = m == -INFINITY ? 0.0f : m;
         l *= alpha;
         const bool big = __any_sync(0xffffffffu, fabsf(m_use) > kBigScore);
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          load(c);
-          uint32_t pk[32];
+        uint32_t pk[32];
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const float4 sc = scl[4 * c + b];
-            float f = fmaxf(rowf * sc.x, kTinyFactor), cb = sc.y - m_use + kShift;
-            if (big) {
+        for (int b = 0; b < 4; ++b) {
+          const float4 sc = scl[b];
+          float f = fb[b], cb = sc.y - m_use + kShift;
+          if (big) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                x[16 * b + e] = __float_as_uint(fmaf(__uint_as_float(x[16 * b + e]), f, sc.y) - m_use + kShift);
-              f = 1.0f;
-              cb = 0.0f;
-            }
-            const uint64_t f2 = pair64(f, f), c2 = pair64(cb, cb);
-            uint64_t sum0 = 0, sum1 = 0;
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              float y0, y1;
-              unpair64(fma2(pair64(__uint_as_float(x[16 * b + e]), __uint_as_float(x[16 * b + e + 1])), f2, c2), y0, y1);
-              const float p0 = ex2(y0), p1 = ex2(y1);
-              uint64_t& sum = e & 2 ? sum1 : sum0;
-              sum = add2(sum, pair64(p0, p1));
-              pk[8 * b + e / 2] = pack_f16(p0, p1);
-            }
-            float s0, s1;
-            unpair64(add2(sum0, sum1), s0, s1);
-            l = fmaf(s0 + s1, sc.z, l);
+            for (int e = 0; e < 16; ++e)
+              x[16 * b + e] = __float_as_uint(fmaf(__uint_as_float(x[16 * b + e]), f, sc.y) - m_use + kShift);
+            f = 1.0f;
+            cb = 0.0f;
           }
-          tcx::tmem_st32(tS + 32u * c, pk);   // P_u(j), keys 64 c .. + 63: over columns of S that were read
+          const uint64_t f2 = pair64(f, f), c2 = pair64(cb, cb);
+          uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            float y0, y1;
+            unpair64(fma2(pair64(__uint_as_float(x[16 * b + e]), __uint_as_float(x[16 * b + e + 1])), f2, c2), y0, y1);
+            const float p0 = ex2(y0), p1 = ex2(y1);
+            uint64_t& sum = e & 2 ? sum1 : sum0;
+            sum = add2(sum, pair64(p0, p1));
+            pk[8 * b + e / 2] = pack_f16(p0, p1);
+          }
+          float s0, s1;
+          unpair64(add2(sum0, sum1), s0, s1);
+          l = fmaf(s0 + s1, sc.z, l);
         }
-        if (j >= 1 && __any_sync(0xffffffffu, rescale)) {
+        tcx::tmem_st32(tX, pk);
+        if (t >= 1 && __any_sync(0xffffffffu, rescale)) {
+          // PV_u(t-1) is the last MMA on O_u before this thread's P_u(t) lets the next one start
+          wait(B_O_DONE + u, uint32_t(t - 1) & 1u, 15u);
+          tcx::tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t o[32];
@@ -546,14 +560,16 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
           }
         }
         tcx::tmem_st_wait();
-        // the MMA thread issues PV_u(j) and S_u(j+1) on this signal alone
-        wait(B_V_FULL + (j & 1), uint32_t(j >> 1) & 1u, 14u);
-        if (j + 1 < nu) wait(B_K_FULL + ((j + 1) & 1), uint32_t((j + 1) >> 1) & 1u, 14u);
+        // the MMA warp issues PV_u(t), and after it S_u(t+2), on this signal alone
+        if (!(t & 1)) {
+          wait(B_V_FULL + (j & 1), uint32_t(j >> 1) & 1u, 14u);
+          if (t + 2 < steps) wait(B_K_FULL + ((j + 1) & 1), uint32_t((j + 1) >> 1) & 1u, 14u);
+        }
         tcx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tcx::mbar_arrive(bar(B_P_FULL + u));
+        if (lane == 0) tcx::mbar_arrive(bar(B_P_FULL + 2 * u + (t & 1)));
       }
-      wait(B_O_DONE + u, uint32_t(nu - 1) & 1u, 13u);
+      wait(B_O_LAST + u, 0u, 13u);
       tcx::tc_fence_after();
       if (a.splits == 1) {
         // O / l -> bf16, staged in Q_u (every S_u MMA completed before the last PV_u), stored coalesced
@@ -573,12 +589,15 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
         }
         tcx::tc_fence_before();
         named_sync(1 + u, BM);
-        const int cc = r & 15;
+        const int cc = r & 15, tok0 = Ru / a.G, rem = Ru - tok0 * a.G;
+        const uint32_t rcp = 65536u / uint32_t(a.G) + 1u;   // x / G = x * rcp >> 16 for x < 144, G <= 16
+        bf16* base = a.out + ((int64_t(rw.qs) + tok0) * a.nh + g * a.G) * HD + 8 * cc;
 #pragma unroll 4
         for (int it = 0; it < BM / 8; ++it) {
           const int rr = it * 8 + (r >> 4);
+          const int dt = int((uint32_t(rem + rr) * rcp) >> 16);
           if (Ru + rr < rw.n)
-            *reinterpret_cast<uint4*>(a.out + rw.id(a, Ru + rr, g) * HD + 8 * cc) =
+            *reinterpret_cast<uint4*>(base + (int64_t(dt) * a.nh + (rem + rr - dt * a.G)) * HD) =
                 *reinterpret_cast<const uint4*>(sQ + tile_off(rr, cc));
         }
       } else {
