@@ -274,6 +274,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
   float sk = 0.0f, sv = 0.0f;            // lanes 0, 1: scales of the warp's two blocks
   int64_t row0 = -1;                     // cache row of the warp's first key
   bool has[2] = {false, false};          // its two blocks are seen by some row and have a page
+  int page = -1;                         // block table entry of the tile after the one in row0
+  auto fetch_page = [&](int j) {         // its load is in flight until the next find()
+    const int blk = (tile_key(j) + 32 * w) / a.c.block_size;
+    page = j < n_kv && blk < a.c.max_blocks ? a.c.table[int64_t(s) * a.c.max_blocks + blk] : -1;
+  };
   auto find = [&](int j) {
     const int key0 = tile_key(j) + 32 * w;
 #pragma unroll
@@ -281,9 +286,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
       const int k = key0 + 16 * b;
       has[b] = max(k, lo_cta) < min(k + 16, hi_cta) || k < min(a.n_sink, hi_cta);
     }
-    row0 = has[0] || has[1] ? row_of(a.c.table, a.c.max_blocks, a.c.block_size, a.c.num_slots, s, key0) : -1;
-    if (row0 < 0) has[0] = has[1] = false;
-    if (row0 + 16 >= a.c.num_slots) has[1] = false;   // (the cache may end inside a page, after a whole block)
+    row0 = int64_t(page) * a.c.block_size + key0 % a.c.block_size;
+    // (the cache may end inside a page, after a whole block)
+    has[0] = has[0] && page >= 0 && row0 < a.c.num_slots;
+    has[1] = has[1] && page >= 0 && row0 + 16 < a.c.num_slots;
   };
   auto load = [&](uint4 (&x)[8], const void* cache) {
     const uint8_t* base = static_cast<const uint8_t*>(cache) + (row0 + rsub) * row_bytes + int64_t(g) * HD + 16 * c4;
@@ -311,16 +317,20 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
   float rowf = 0.0f;
   if (warp >= 8) {
     uint4 x[16];
-    float top = 0.0f;
 #pragma unroll
     for (int c = 0; c < 16; ++c)
       x[c] = valid ? *reinterpret_cast<const uint4*>(a.q + id * HD + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+    // largest magnitude, two bf16 at a time (bit patterns without the sign order like the values)
+    uint32_t t2[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int c = 0; c < 16; ++c) {
-      const uint32_t wd[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(wd[e])), fabsf(bf16_hi(wd[e]))));
+      t2[0] = __vmaxu2(t2[0], x[c].x & 0x7fff7fffu);
+      t2[1] = __vmaxu2(t2[1], x[c].y & 0x7fff7fffu);
+      t2[2] = __vmaxu2(t2[2], x[c].z & 0x7fff7fffu);
+      t2[3] = __vmaxu2(t2[3], x[c].w & 0x7fff7fffu);
     }
+    const uint32_t tm = __vmaxu2(__vmaxu2(t2[0], t2[1]), __vmaxu2(t2[2], t2[3]));
+    const float top = __uint_as_float(max(tm << 16, tm & 0xffff0000u));
     float mul, inv;
     row_scale(top, mul, inv);
     mul *= a.q_sign;
@@ -332,7 +342,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
     }
     tcx::fence_proxy_async();
   } else if (warp >= 4) {
+    fetch_page(0);
     find(0);
+    fetch_page(1);
     load_scales();
     load(kr, a.c.k);
     load(vr, a.c.v);
@@ -453,6 +465,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
       publish(B_K_FULL + slot);
       if (j + 1 < n_kv) {
         find(j + 1);
+        fetch_page(j + 2);
         load_scales();
         load(kr, a.c.k);
       }
