@@ -131,6 +131,11 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ uint64_t pair64(float a, float b) {
   uint64_t d;
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
@@ -511,14 +516,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
         float fb[4], m_step = -INFINITY;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          float mx[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(x[16 * b + e]);
-#pragma unroll
-          for (int e = 4; e < 16; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(x[16 * b + e]));
+          const uint32_t* y = x + 16 * b;
+          auto f = [&](int e) { return __uint_as_float(y[e]); };
+          const float mx = max3(max3(max3(f(0), f(1), f(2)), max3(f(3), f(4), f(5)), max3(f(6), f(7), f(8))),
+                                max3(max3(f(9), f(10), f(11)), max3(f(12), f(13), f(14)), f(15)), -INFINITY);
           const float4 sc = scl[b];
           fb[b] = fmaxf(rowf * sc.x, kTinyFactor);
-          m_step = fmaxf(m_step, fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fb[b], sc.y));
+          m_step = fmaxf(m_step, fmaf(mx, fb[b], sc.y));
         }
         float alpha = 1.0f;
         bool rescale = false;
