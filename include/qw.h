@@ -302,11 +302,11 @@ int qw_attention_prefill_paged(const void* q, const void* k_cache, const void* v
  * half the bytes).  The four entry points share these arguments:
  *   k_cache, v_cache  one-byte codes [num_slots, nkv, 128], 16-byte aligned;
  *       kv_dtype QW_I8 (codes -127 .. 127) or QW_E4M3 (the e4m3 patterns that
- *       stand for NaN are never written and read as +-480)
+ *       stand for NaN are never written; rows behind a sequence may hold them)
  *   k_scale, v_scale  float [num_slots / scale_block, nkv]: the scale of each
  *       aligned block of scale_block rows (16, 32 or 64; num_slots a multiple
- *       of it) and kv head.  An element's value is code * scale; a scale below
- *       2^-100 counts as 0.
+ *       of it) and kv head, at least 0.  An element's value is code * scale; a
+ *       scale below 2^-100 counts as 0 in attention.
  *   block_table int32 [n_seqs, max_blocks], block_size (a multiple of 64): as
  *       for the paged entry points.  Keys whose page is negative, beyond the
  *       table or outside [0, num_slots) read as zeros and are not written.

@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(DK_THREADS, 1) attn_decode_kv8_kernel(const __
         qb[n][e][0] = pack_f16(f[4 * e] * mul, f[4 * e + 1] * mul);
         qb[n][e][1] = pack_f16(f[4 * e + 2] * mul, f[4 * e + 3] * mul);
       }
-      inv *= a.scale_log2 * pair_factor<KV>();
+      inv *= a.scale_log2;
       qa[n][0] = __shfl_sync(0xffffffffu, inv, 8 * tq);
       qa[n][1] = __shfl_sync(0xffffffffu, inv, 8 * tq + 4);
     }
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(DK_THREADS, 1) attn_decode_kv8_kernel(const __
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
           const uint32_t sK = ring + uint32_t(st[u]) * DK_STAGE + uint32_t(warp) * DK_SUB;
-          // a tile that is not there: any codes (all finite), no visible key
+          // a tile that is not there has no visible key, whatever codes are read
           const float* sc = scales + st[u] * 2 * DK_WARPS + warp;
           sk[u] = act[u] ? sc[0] : 0.0f;
           const float sv = act[u] ? sc[DK_WARPS] : 1.0f;
@@ -426,7 +426,12 @@ __global__ void __launch_bounds__(DK_THREADS, 1) attn_decode_kv8_kernel(const __
           for (int r = 0; r < 4; ++r) {
             const int row = 2 * tq + (r & 1) + 8 * (r >> 1);
             const uint4 x = lds128(sV + uint32_t(row) * 128u + (uint32_t(gq ^ (row & 7)) << 4));
-            v[r][0] = x.x; v[r][1] = x.y; v[r][2] = x.z; v[r][3] = x.w;
+            // (a row that is not there may hold any code, NaN too: 0 * V has to stay 0)
+            const bool there = act[u] && key0[u] + row < sp.L;
+            v[r][0] = there ? x.x : 0u;
+            v[r][1] = there ? x.y : 0u;
+            v[r][2] = there ? x.z : 0u;
+            v[r][3] = there ? x.w : 0u;
           }
           // O^T rows: tile d holds dims 16 gq + 2 d (row gq) and 16 gq + 2 d + 1 (row gq + 8)
 #pragma unroll
@@ -516,7 +521,7 @@ __global__ void __launch_bounds__(DK_THREADS, 1) attn_decode_kv8_kernel(const __
           const int hd = 8 * n + 2 * tq + e;
           if (hd >= a.G) continue;
           float f[16];
-          const float fac = split ? 1.0f : (l[n][e] > 0.0f ? kUnshift * pair_factor<KV>() / l[n][e] : 0.0f);
+          const float fac = split ? 1.0f : (l[n][e] > 0.0f ? kUnshift / l[n][e] : 0.0f);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             f[2 * i] = o[n][i][e] * fac;
@@ -587,7 +592,7 @@ __global__ void __launch_bounds__(DK_THREADS, 1) attn_decode_kv8_kernel(const __
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               if (h0 + u >= a.G) continue;
-              const float fac = lsum[u] > 0.0f ? kUnshift * pair_factor<KV>() / lsum[u] : 0.0f;
+              const float fac = lsum[u] > 0.0f ? kUnshift / lsum[u] : 0.0f;
               *reinterpret_cast<uint2*>(a.out + (int64_t(b) * a.nh + g * a.G + h0 + u) * HD + 4 * lane) =
                   make_uint2(pack_bf16(acc[u].x * fac, acc[u].y * fac), pack_bf16(acc[u].z * fac, acc[u].w * fac));
             }

@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
     float mul, inv;
     row_scale(top, mul, inv);
     mul *= a.q_sign;
-    rowf = inv * a.scale_log2 * pair_factor<KV>();
+    rowf = inv * a.scale_log2;
 #pragma unroll
     for (int c = 0; c < 16; ++c) {
       auto cv = [&](uint32_t v) { return pack_f16(bf16_lo(v) * mul, bf16_hi(v) * mul); };
@@ -455,6 +455,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
       bool zero_v[2];   // blocks whose v_scale counts as zero
 #pragma unroll
       for (int b = 0; b < 2; ++b) zero_v[b] = !(__shfl_sync(0xffffffffu, sv, b) >= kTinyScale);
+      const int tail_key = tile_key(j) + 32 * w + rsub;
+      const bool past_end = tile_key(j) + 32 * w + 32 > hi_cta;
       const bool seen = lane ? has[1] : has[0];
       const int key0 = tile_key(j) + 32 * w + 16 * (lane & 1);
       // a block without a page counts as zero keys; one that no row sees is left out
@@ -478,6 +480,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (zero_v[i >> 2]) vr[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (past_end) {   // rows that no query sees may hold any code, NaN too: 0 * V has to stay 0
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (tail_key + 8 * (i >> 1) >= hi_cta) vr[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
       store(vr, OFF_V + uint32_t(slot) * TILE);
       publish(B_V_FULL + slot);
       if (j + 1 < n_kv) load(vr, a.c.v);
@@ -590,7 +597,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
       tcx::tc_fence_after();
       if (a.splits == 1) {
         // O / l -> bf16, staged in Q_u (every S_u MMA completed before the last PV_u), stored coalesced
-        const float inv = l > 0.0f ? kUnshift * pair_factor<KV>() / l : 0.0f;
+        const float inv = l > 0.0f ? kUnshift / l : 0.0f;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t o[32];
@@ -619,7 +626,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
         }
       } else {
         const int64_t at = split * n_rows_all + id;
-        const float fac = kUnshift * pair_factor<KV>();
+        const float fac = kUnshift;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t o[32];

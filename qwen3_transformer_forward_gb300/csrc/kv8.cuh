@@ -3,9 +3,9 @@
 //
 // A cache row (one token) holds n_kv_heads x 128 one-byte codes; every aligned
 // block of `scale_block` rows has one fp32 scale for each kv head, and an
-// element's value is code * scale.  Codes are int8 in [-127, 127] or e4m3; the
-// two e4m3 bit patterns that stand for NaN are never written, and are read as
-// +-480, so that whatever a recycled page holds is finite.
+// element's value is code * scale.  Codes are int8 in [-127, 127] or e4m3 (the two
+// e4m3 bit patterns that stand for NaN are never written, but a recycled page may
+// hold them behind a sequence's end: the attention kernels clear those V rows).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -24,15 +24,15 @@ constexpr float kTinyScale = 7.888609052210118e-31f;   // 2^-100
 // KV: QW_I8 or QW_E4M3
 template <int KV> __device__ constexpr float code_max() { return KV == QW_I8 ? 127.0f : 448.0f; }
 
-// The e4m3 bits placed in an f16 give the value times 2^-8 (the exponent biases
-// are 7 and 15); exact for every code, subnormals included.
-__device__ __forceinline__ float code_f32_e4m3(uint32_t b) {
-  const uint32_t h = ((b & 0x80u) << 8) | ((b & 0x7fu) << 7);
-  return __half2float(__ushort_as_half(static_cast<unsigned short>(h))) * 256.0f;
+// Two e4m3 codes (low 16 bits) as an f16 pair; exact for every code, subnormals included.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t w) {
+  uint32_t d;
+  asm("{\n .reg .b16 x, y;\n mov.b32 {x, y}, %1;\n cvt.rn.f16x2.e4m3x2 %0, x;\n}" : "=r"(d) : "r"(w));
+  return d;
 }
 template <int KV> __device__ __forceinline__ float code_f32(uint32_t b) {
   if constexpr (KV == QW_I8) return float(int(b << 24) >> 24);
-  else return code_f32_e4m3(b);
+  else return __half2float(__ushort_as_half(static_cast<unsigned short>(e4m3_pair(b) & 0xffffu)));
 }
 // four codes of a word
 template <int KV> __device__ __forceinline__ void codes_f32(uint32_t w, float* f) {
@@ -119,13 +119,10 @@ inline int check_table(const char* who, const int32_t* table, int max_blocks, in
 
 // ---------------------------------------------------------------------------
 // codes as f16 pairs for the matrix instructions: every int8 and e4m3 code is
-// exact in f16.  e4m3 pairs come out times 2^-8 (code_f32_e4m3), a factor that
-// the kernels fold into the scores and the output.
+// exact in f16
 // ---------------------------------------------------------------------------
 namespace qw {
 namespace kv8 {
-
-template <int KV> __device__ constexpr float pair_factor() { return KV == QW_I8 ? 1.0f : 256.0f; }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t d;
@@ -144,22 +141,15 @@ template <int KV> __device__ __forceinline__ void word_pairs(uint32_t w, uint32_
     const uint32_t u = w ^ 0x80808080u;
     p01 = unbias(prmt(u, 0x64646464u, 0x4140));   // f16 0x6400 | u = 1024 + u
     p23 = unbias(prmt(u, 0x64646464u, 0x4342));
-  } else {   // sign-extend each byte to 16 bits, exponent and mantissa to bits 13 .. 7
-    p01 = (prmt(w, 0u, 0x9180) << 7) & 0xbf80bf80u;
-    p23 = (prmt(w, 0u, 0xb3a2) << 7) & 0xbf80bf80u;
+  } else {   // (one conversion: shifts and masks that leave out the NaN patterns took three instructions)
+    p01 = e4m3_pair(w);
+    p23 = e4m3_pair(w >> 16);
   }
 }
 // Codes i of words a and b side by side, i = 0 .. 3.
 template <int KV> __device__ __forceinline__ void cross_pairs(uint32_t a, uint32_t b, uint32_t (&p)[4]) {
-  if constexpr (KV == QW_I8) {
-    word_pairs<KV>(prmt(a, b, 0x5140), p[0], p[1]);
-    word_pairs<KV>(prmt(a, b, 0x7362), p[2], p[3]);
-  } else {
-    p[0] = (prmt(a, b, 0xc480) << 7) & 0xbf80bf80u;
-    p[1] = (prmt(a, b, 0xd591) << 7) & 0xbf80bf80u;
-    p[2] = (prmt(a, b, 0xe6a2) << 7) & 0xbf80bf80u;
-    p[3] = (prmt(a, b, 0xf7b3) << 7) & 0xbf80bf80u;
-  }
+  word_pairs<KV>(prmt(a, b, 0x5140), p[0], p[1]);
+  word_pairs<KV>(prmt(a, b, 0x7362), p[2], p[3]);
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
