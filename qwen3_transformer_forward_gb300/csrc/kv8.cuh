@@ -40,8 +40,8 @@ template <int KV> __device__ __forceinline__ void codes_f32(uint32_t w, float* f
   for (int i = 0; i < 4; ++i) f[i] = code_f32<KV>((w >> (8 * i)) & 0xffu);
 }
 
-// Four values already divided by their scale -> codes: round to nearest even,
-// clamped to the largest code; NaN becomes 0.
+// Four values already divided by their scale, none of them NaN -> codes: round to
+// nearest even, clamped to the largest code.
 template <int KV> __device__ __forceinline__ uint32_t quant4(const float* x) {
   if constexpr (KV == QW_I8) {
     uint32_t w = 0;
@@ -49,11 +49,8 @@ template <int KV> __device__ __forceinline__ uint32_t quant4(const float* x) {
     for (int i = 0; i < 4; ++i) w |= (uint32_t(min(max(__float2int_rn(x[i]), -127), 127)) & 0xffu) << (8 * i);
     return w;
   } else {
-    float y[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = x[i] == x[i] ? x[i] : 0.0f;
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3);
     return lo | (hi << 16);
   }
 }
