@@ -256,8 +256,10 @@ template <int KV> __device__ __forceinline__ uint4 requant(const uint4& c, float
 // A block's tokens meet in one CTA because they share a scale: the block maxima of
 // k and of v are formed in shared memory and every value is quantised from the
 // registers that it was computed in, so each input is read once.  k and v
-// together, and several q heads on one RoPE row, keep enough loads in flight:
-// 8 x 2048 tokens took 83 us with one of them at a time.
+// together, and two q heads on one RoPE row, keep enough loads in flight: 8 x 2048
+// tokens of 16 q and 8 kv heads take 55.7 us, 4.2 TB/s (83 us with one of them at a
+// time; four q heads 65 us, one 61 us, 1024 threads an SM in each).  Bounded by the
+// issue of the norm, rotation and quantiser, about 20 instructions an element.
 constexpr int QH = 2;
 template <int KV, int SB>
 __global__ void __launch_bounds__(SB * 8, 1024 / (SB * 8)) kv8_append_kernel(const AppendArgs a) {
@@ -486,9 +488,10 @@ int launch_append(const AppendArgs& a0, cudaStream_t st) {
   // every touched block holds at least one new token, and a sequence with Lq of
   // them touches at most (Lq + sb - 2) / sb + 1 blocks
   const int64_t blocks = std::min(a.T, a.T / SB + 2 * int64_t(a.n_seqs));
-  // up to four tokens a sequence on average: warps instead of CTAs (64 sequences of
-  // one token: 4.9 us against 14 us; 16 sequences of 8: 8.9 us against 6.6 us)
-  const bool few = a.T <= 4 * int64_t(a.n_seqs);
+  // Up to eight tokens a sequence on average: warps instead of CTAs.  16 q and 8 kv
+  // heads, scale_block 64: 64 sequences of one token 3.4 us against 7.4, of eight 5.8
+  // against 11.3, 16 sequences of eight 4.2 against 4.1, of sixteen 6.4 against 5.0.
+  const bool few = a.T <= 8 * int64_t(a.n_seqs);
   a.kv_ctas = few ? (blocks * a.nkv * 2 + 3) / 4 : blocks * a.nkv;
   const int64_t q_ctas = few ? (a.T * a.nh + 15) / 16 : (a.T * ((a.nh + QH - 1) / QH) + SB - 1) / SB;
   if (a.T * (a.nh + 2 * int64_t(a.nkv)) > (int64_t(1) << 30) || blocks * a.nkv > (int64_t(1) << 28))
