@@ -5,14 +5,16 @@
 // q head R % G of its group of G, so that any group size fills the 128-row units
 // and a short prompt wastes few rows.  One CTA owns two units (256 rows) and
 // walks the key tiles (128 keys) that any of its rows sees.  Per CTA (16 warps):
-//   warp 0        allocates 512 TMEM columns and issues every MMA from one thread:
-//                   S_u  = Q_u K_j^T   A = Q_u (smem), B = K_j (smem), both K-major
-//                   O_u += P_u V_j     A = P_u (TMEM), B = V_j (smem, MN-major)
-//                 in the order PV_0(j), S_0(j+1), PV_1(j), S_1(j+1)
+//   warp 0        allocates 512 TMEM columns and issues every MMA from one lane, in
+//                 steps of 64 keys (two a tile), S double-buffered in each unit:
+//                   S_u(t)  = Q_u K^T   A = Q_u (smem), B = K (smem), both K-major
+//                   O_u    += P_u(t) V  A = P_u (TMEM), B = V (smem, MN-major)
+//                 in the order PV_0(t), PV_1(t), S_0(t+2), S_1(t+2): a unit's softmax
+//                 works on step t + 1 while the tensor pipe serves both
 //   warps 4-7     read the codes of K_j and V_j from the cache into registers one
 //                 tile ahead, convert them to f16 (exact) and store them as
-//                 128-byte-swizzled operand tiles, two slots each: 1.25 to 1.5
-//                 instructions an element, once for the 256 rows of both units
+//                 128-byte-swizzled operand tiles, two slots each: once for the 256
+//                 rows of both units
 //   warps 8-11    softmax of unit 0, warps 12-15 of unit 1: one row per thread
 // Block scales never touch the operands.  A block of 16 keys shares one scale,
 // so with x = score * log2 e * k_scale + log2(v_scale) the running maximum m is
@@ -22,10 +24,17 @@
 // power of two per row (row_scale), exact in f16.  k_scale >= 0 and the softmax
 // scale's sign sits in q, so a block's largest x belongs to its largest score:
 // the maximum is taken over the raw scores.
-// TMEM columns: S_0/P_0 [0,128), S_1/P_1 [128,256), O_0 [256,384), O_1 [384,512).
+// TMEM columns: S of unit u at 128 u + 64 (t & 1), P over the first half of its S;
+// O_0 [256,384), O_1 [384,512).
 // Few rows over many keys: the tiles are cut into `splits` shares (host rule in
 // prefill_splits), each CTA leaves (m, l, O) in fp32 and a second kernel adds them
 // in order.
+// Bound: a tile of 128 keys takes about 4600 cycles a CTA against 2560 of tensor
+// pipe; the softmax's dependent steps (two warps on an SM sub-partition) and the
+// operand traffic through shared memory (Q is read again for each step, K and V are
+// written by the converters: about 2600 cycles of its bandwidth) hold it there.
+// 8 x 2048 tokens, 16 q / 8 kv heads, int8: 215 us, 640 TFLOP/s; 2 x 2500 new tokens
+// over 24000, 32 / 8 heads, e4m3, window 8192: 639 us, 960 TFLOP/s.
 // Every mbarrier wait is bounded (2 s); on timeout the kernel records an error
 // word and runs to its end without waiting further.
 #include <math.h>
@@ -78,9 +87,8 @@ __device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sy
 // One MMA step, issued by the lane with `lead`.  Descriptors come as their low
 // words (the start address moves, the rest is one constant for each layout), and
 // the lead is a predicate, not a branch: the issuing warp stays convergent and its
-// operands in uniform registers.  (Building each 64-bit descriptor inside an
-// `if (lane == 0)` took the issuing thread 5600 cycles a key tile, against 2050 of
-// tensor pipe work.)
+// operands in uniform registers (8 x 2048 tokens: 313 -> 298 us against building each
+// 64-bit descriptor inside an `if (lane == 0)`).
 __device__ __forceinline__ void umma_ss(uint32_t lead, uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
                                         uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -129,6 +137,23 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
         "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
         "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
       : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {   // arrived
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      " tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -511,14 +536,25 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
         const uint32_t tX = tS + uint32_t(t & 1) * 64u;   // S_u(t), then P_u(t) over its first 32 columns
         wait(B_S_FULL + 2 * u + (t & 1), uint32_t(t >> 1) & 1u, 12u);
         tcx::tc_fence_after();
-        uint32_t x[64];
-        tmem_ld64(tX, x);
         const int k0 = tile_key(j) + HALF * (t & 1);
         const int end = hi - k0, beg = lo_row - k0, snk = a.n_sink - k0;   // columns [beg, end) and [0, min(snk, end))
-        if (!(HALF <= end && (0 >= beg || HALF <= snk)))
+        // A masked step writes -inf into S first.  Rare paths are short loops over TMEM, not
+        // unrolled over the registers of S: they would sit in the middle of the loop's code
+        // (222 -> 215 us for 8 x 2048 tokens).
+        if (__any_sync(0xffffffffu, !(HALF <= end && (0 >= beg || HALF <= snk)))) {
+#pragma unroll 1
+          for (int c = 0; c < HALF; c += 16) {
+            uint32_t y[16];
+            tmem_ld16(tX + c, y);
 #pragma unroll
-          for (int e = 0; e < HALF; ++e)
-            if (!(e < end && (e >= beg || e < snk))) x[e] = __float_as_uint(-INFINITY);
+            for (int e = 0; e < 16; ++e)
+              if (!(c + e < end && (c + e >= beg || c + e < snk))) y[e] = __float_as_uint(-INFINITY);
+            tmem_st16(tX + c, y);
+          }
+          tcx::tmem_st_wait();
+        }
+        uint32_t x[64];
+        tmem_ld64(tX, x);
         const float4* scl = reinterpret_cast<const float4*>(sm + OFF_SCL) + (j & 3) * 8 + 4 * (t & 1);
         float fb[4], m_step = -INFINITY;
 #pragma unroll
@@ -541,18 +577,28 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
         const float m_use = m == -INFINITY ? 0.0f : m;
         l *= alpha;
         const bool big = __any_sync(0xffffffffu, fabsf(m_use) > kBigScore);
+        float unit = 1.0f;   // 0: x holds the exponents already
+        if (big) {
+#pragma unroll 1
+          for (int b = 0; b < 4; ++b) {
+            uint32_t y[16];
+            tmem_ld16(tX + 16u * b, y);
+            const float4 sc = scl[b];
+            const float f = fmaxf(rowf * sc.x, kTinyFactor);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              y[e] = __float_as_uint(fmaf(__uint_as_float(y[e]), f, sc.y) - m_use + kShift);
+            tmem_st16(tX + 16u * b, y);
+          }
+          tcx::tmem_st_wait();
+          tmem_ld64(tX, x);
+          unit = 0.0f;
+        }
         uint32_t pk[32];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           const float4 sc = scl[b];
-          float f = fb[b], cb = sc.y - m_use + kShift;
-          if (big) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              x[16 * b + e] = __float_as_uint(fmaf(__uint_as_float(x[16 * b + e]), f, sc.y) - m_use + kShift);
-            f = 1.0f;
-            cb = 0.0f;
-          }
+          const float f = big ? 1.0f : fb[b], cb = unit * (sc.y - m_use + kShift);
           const uint64_t f2 = pair64(f, f), c2 = pair64(cb, cb);
           uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
