@@ -277,19 +277,23 @@ def attention_prefill_paged(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, blo
         n_kv_heads, head_dim, scale, _dev_ptr(out, "out"), dtype_code(q.dtype), _stream(stream)))
 
 
+_KV_CODES = {torch.int8: QW_I8, torch.float8_e4m3fn: QW_E4M3}
+
+
 def kv_code(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
             scale_block: int) -> int:
     """kv_dtype of an 8-bit cache; the library sees pointers only, so the tensors' types and sizes are checked here."""
-    if k_cache.dtype not in (torch.int8, torch.float8_e4m3fn) or v_cache.dtype != k_cache.dtype:
+    code = _KV_CODES.get(k_cache.dtype)
+    if code is None or v_cache.dtype != k_cache.dtype:
         raise QwError(QW_ERR_DTYPE, f"caches must both be int8 or float8_e4m3fn, not {k_cache.dtype} and {v_cache.dtype}")
     if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
         raise QwError(QW_ERR_DTYPE, "scales must be float32")
-    slots, nkv = k_cache.shape[0], k_cache.shape[1]
-    if v_cache.shape != k_cache.shape or scale_block <= 0 or any(
-            tuple(t.shape) != (slots // scale_block, nkv) for t in (k_scale, v_scale)):
-        raise QwError(QW_ERR_SHAPE, f"caches {tuple(k_cache.shape)} and {tuple(v_cache.shape)} need scales of "
-                                    f"[{slots} / {scale_block}, {nkv}]")
-    return QW_I8 if k_cache.dtype == torch.int8 else QW_E4M3
+    shape = k_cache.shape
+    want = (shape[0] // scale_block if scale_block > 0 else -1, shape[1])
+    if v_cache.shape != shape or k_scale.shape != want or v_scale.shape != want:
+        raise QwError(QW_ERR_SHAPE, f"caches {tuple(shape)} and {tuple(v_cache.shape)} need scales of {want}, not "
+                                    f"{tuple(k_scale.shape)} and {tuple(v_scale.shape)}")
+    return code
 
 
 def kv8_append(qkv, n_heads, n_kv_heads, head_dim, tp, positions, cos_sin, q_gamma, k_gamma, eps, cu_seqlens_q,
@@ -334,6 +338,10 @@ def attention_decode_kv8(q, k_cache, v_cache, k_scale, v_scale, scale_block, con
         _dev_ptr(block_table, "block_table"), block_table.shape[1], block_size, q.shape[0], max_context, n_heads,
         n_kv_heads, head_dim, scale, window, n_sink, _dev_ptr(out, "out"), _dev_ptr(workspace, "workspace"), ws_bytes,
         dtype_code(q.dtype), kv, _stream(stream)))
+
+
+# the largest workspace that attention_prefill_kv8 asks for (total_q <= n_seqs * max_seqlen_q)
+ATTENTION_PREFILL_KV8_WORKSPACE_MAX = 64 * 1024 + 152 * 256 * 130 * 4
 
 
 def attention_prefill_kv8_workspace_size(n_seqs, total_q, max_seqlen_q, max_context, n_heads, n_kv_heads) -> int:

@@ -781,7 +781,7 @@ extern "C" size_t qw_attention_prefill_kv8_workspace_size(int n_seqs, int64_t to
                                                           int max_context, int n_heads, int n_kv_heads) {
   if (n_seqs <= 0 || total_q <= 0 || max_seqlen_q <= 0 || max_context < 0 || n_heads <= 0 || n_kv_heads <= 0) return 0;
   const int s = kv8p::prefill_splits(n_seqs, max_seqlen_q, max_context, n_heads, n_kv_heads);
-  return s == 1 ? 0 : size_t(s) * size_t(total_q) * n_heads * (kv8::HD + 2) * sizeof(float);
+  return s == 1 ? 0 : kCounterBytes + size_t(s) * size_t(total_q) * n_heads * (kv8::HD + 2) * sizeof(float);
 }
 
 extern "C" int qw_attention_prefill_kv8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -828,7 +828,7 @@ extern "C" int qw_attention_prefill_kv8(const void* q, const void* k_cache, cons
   a.scale_log2 = fabsf(scale) * kv8p::kLog2e;
   a.q_sign = scale < 0.0f ? -1.0f : 1.0f;
   a.out = static_cast<bf16*>(out);
-  a.ws_o = static_cast<float*>(workspace);
+  a.ws_o = need > 0 ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterBytes) : nullptr;   // (no counters here)
   a.ws_ml = need > 0 ? a.ws_o + size_t(a.splits) * size_t(total_q) * n_heads * kv8::HD : nullptr;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return kv_dtype == QW_I8 ? kv8p::launch<QW_I8>(a, n_seqs, st) : kv8p::launch<QW_E4M3>(a, n_seqs, st);

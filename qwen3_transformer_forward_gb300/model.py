@@ -95,6 +95,21 @@ def load_params(shape, seed: int = 0, device="cuda", n_layers: Optional[int] = N
 # batch descriptions (the get_context() fields, [SK] §6-§7)
 # ----------------------------------------------------------------------------
 
+@dataclass(frozen=True)
+class Kv8Config:
+    """An 8-bit paged KV cache in place of the bf16 one (bf16 models with head_dim 128).
+
+    The contexts of such a model carry a block_table (int32 [S, max_blocks]) and
+    context_lens; slot_mapping and seq_base are not read.  window > 0: every layer
+    sees the last `window` keys and the first n_sink.
+    """
+    kv_dtype: torch.dtype = torch.int8    # or torch.float8_e4m3fn
+    block_size: int = 256
+    scale_block: int = 64
+    window: int = 0
+    n_sink: int = 0
+
+
 @dataclass
 class PrefillContext:
     ids: torch.Tensor            # int64 [T]
@@ -104,6 +119,9 @@ class PrefillContext:
     seq_base: torch.Tensor       # int32 [S]
     last_idx: torch.Tensor       # int32 [S]
     max_seqlen: int
+    block_table: Optional[torch.Tensor] = None    # int32 [S, max_blocks] (8-bit paged cache)
+    context_lens: Optional[torch.Tensor] = None   # int32 [S]: cached keys, the new tokens included
+    max_context: int = 0                          # >= every context_lens
 
     @property
     def n_tokens(self):
@@ -118,6 +136,7 @@ class DecodeContext:
     slot_mapping: torch.Tensor   # int64 [B]
     seq_base: torch.Tensor       # int32 [B]
     max_context: int
+    block_table: Optional[torch.Tensor] = None    # int32 [B, max_blocks] (8-bit paged cache)
 
     @property
     def n_tokens(self):
@@ -142,7 +161,8 @@ class Qwen3Forward:
     """Device buffers + the sequence of libqw calls for prefill and decode."""
 
     def __init__(self, shape, params: ModelParams, max_tokens: int, num_slots: int, max_seqs: int,
-                 max_context: int, device="cuda", kv_caches=None):
+                 max_context: int, device="cuda", kv_caches=None, kv8: Optional[Kv8Config] = None):
+        """kv_caches: (k, v), lists of one tensor per layer; with kv8 (k, v, k_scale, v_scale)."""
         self.m = shape
         self.p = params
         self.device = device
@@ -165,7 +185,19 @@ class Qwen3Forward:
         self.next_tokens = torch.empty(max(max_seqs, T), dtype=torch.int64, device=device)
         self.err = torch.zeros(1, dtype=torch.int32, device=device)
         nl = len(params.layers)
-        if kv_caches is None:
+        self.kv8 = kv8
+        self.k_scale, self.v_scale = [], []
+        if kv8 is not None:
+            if dt != torch.bfloat16 or hd != 128:
+                raise ValueError("the 8-bit KV cache is for bf16 models with head_dim 128")
+            if kv_caches is None:
+                codes = lambda: [torch.zeros(num_slots, shape.n_kv_heads, hd, dtype=torch.int8,  # noqa: E731
+                                             device=device).view(kv8.kv_dtype) for _ in range(nl)]
+                scales = lambda: [torch.zeros(num_slots // kv8.scale_block, shape.n_kv_heads, dtype=torch.float32,  # noqa: E731
+                                              device=device) for _ in range(nl)]
+                kv_caches = codes(), codes(), scales(), scales()
+            self.k_cache, self.v_cache, self.k_scale, self.v_scale = kv_caches
+        elif kv_caches is None:
             self.k_cache = [torch.zeros(num_slots, shape.n_kv_heads, hd, dtype=dt, device=device) for _ in range(nl)]
             self.v_cache = [torch.zeros(num_slots, shape.n_kv_heads, hd, dtype=dt, device=device) for _ in range(nl)]
         else:
@@ -175,6 +207,9 @@ class Qwen3Forward:
         for (M, N, K, mode, epi) in self._gemm_shapes(T) + self._gemm_shapes(max(max_seqs, 1)):
             ws = max(ws, L.gemm_workspace_size(M, N, K, tp, mode, epi, dt))
         ws = max(ws, L.attention_decode_workspace_size(max(max_seqs, 1), max_context, shape.n_heads, hd))
+        if kv8 is not None:
+            ws = max(ws, L.attention_decode_kv8_workspace_size(max(max_seqs, 1), max_context, shape.n_heads,
+                                                               shape.n_kv_heads), L.ATTENTION_PREFILL_KV8_WORKSPACE_MAX)
         ws = max(ws, L.lm_head_workspace_size(max(max_seqs, 1), shape.vocab, H, tp, dt))
         # completion counters at its start must be zero before the first call
         self.workspace = torch.zeros(max(ws, 256), dtype=torch.uint8, device=device)
@@ -220,7 +255,7 @@ class Qwen3Forward:
         """Prefill: QK-norm + RoPE + KV store as the QKV GEMM's epilogue (bf16,
         head_dim 128, two whole heads of one shard per 256-column tile)."""
         m = self.m
-        return (self.fused_qkv and self.dtype == torch.bfloat16 and m.head_dim == 128
+        return (self.fused_qkv and self.kv8 is None and self.dtype == torch.bfloat16 and m.head_dim == 128
                 and ((m.n_heads + 2 * m.n_kv_heads) // m.tp) % 2 == 0 and m.hidden % 8 == 0)
 
     def prefill_fusion_ok(self) -> bool:
@@ -229,7 +264,7 @@ class Qwen3Forward:
         RMSNorm in the o_proj and down GEMMs (a row's hidden columns in one
         cluster of 256-column tiles)."""
         m = self.m
-        return (self.fused_prefill and self.dtype == torch.bfloat16 and m.head_dim == 128
+        return (self.fused_prefill and self.kv8 is None and self.dtype == torch.bfloat16 and m.head_dim == 128
                 and ((m.n_heads + 2 * m.n_kv_heads) // m.tp) % 2 == 0 and m.hidden % 256 == 0
                 and m.hidden <= 2048 and (m.n_heads * m.head_dim // m.tp) % 8 == 0
                 and (m.intermediate // m.tp) % 8 == 0 and len(self.p.layers) > 0)
@@ -308,6 +343,8 @@ class Qwen3Forward:
             with self._around(f"{ph}.attention", l):
                 L.attention_prefill(q, self.k_cache[l], self.v_cache[l], ctx.cu_seqlens, ctx.cu_seqlens, ctx.seq_base,
                                     ctx.max_seqlen, m.n_heads, m.n_kv_heads, m.head_dim, self.scale, attn, stream)
+        elif self.kv8 is not None:
+            self._attention_kv8(l, qkv, q, attn, ctx, decode, ph, stream)
         elif decode and self.dtype == torch.bfloat16 and m.head_dim == 128:
             # QK-norm + RoPE + KV store folded into decode attention.  Sequence b's
             # cache is contiguous from seq_base[b] and this step's k/v go to its last
@@ -350,9 +387,29 @@ class Qwen3Forward:
         with self._around(f"{ph}.gemm_down", l):
             L.gemm(act, p.down, h, m.hidden, tp, L.QW_GEMM_ROW_REDUCE, L.QW_EPI_NONE, self.workspace, stream)
 
+    def _attention_kv8(self, l: int, qkv, q, attn, ctx, decode: bool, ph: str, stream=None):
+        """QK-norm + RoPE + quantised append, then attention over the 8-bit paged cache."""
+        m, p, c = self.m, self.p.layers[l], self.kv8
+        if ctx.block_table is None or ctx.context_lens is None:
+            raise ValueError("the 8-bit KV cache needs a context with block_table and context_lens")
+        cache = (self.k_cache[l], self.v_cache[l], self.k_scale[l], self.v_scale[l], c.scale_block)
+        cu = None if decode else ctx.cu_seqlens
+        with self._around(f"{ph}.kv8_append", l):
+            L.kv8_append(qkv, m.n_heads, m.n_kv_heads, m.head_dim, m.tp, ctx.positions, self.cos_sin, p.q_norm, p.k_norm,
+                         m.eps, cu, ctx.context_lens, ctx.block_table, c.block_size, *cache, q, self.err, stream)
+        with self._around(f"{ph}.attention", l):
+            if decode:
+                L.attention_decode_kv8(q, *cache, ctx.context_lens, ctx.block_table, c.block_size, ctx.max_context,
+                                       m.n_heads, m.n_kv_heads, m.head_dim, self.scale, attn, self.workspace, c.window,
+                                       c.n_sink, stream)
+            else:
+                L.attention_prefill_kv8(q, *cache, cu, ctx.context_lens, ctx.block_table, c.block_size, ctx.max_seqlen,
+                                        ctx.max_context, m.n_heads, m.n_kv_heads, m.head_dim, self.scale, attn,
+                                        self.workspace, c.window, c.n_sink, stream)
+
     def fused_decode_ok(self, B: int) -> bool:
         m = self.m
-        if not self.fused_decode or self.dtype != torch.bfloat16 or len(self.p.layers) == 0 or B > self.max_seqs:
+        if not self.fused_decode or self.kv8 is not None or self.dtype != torch.bfloat16 or len(self.p.layers) == 0 or B > self.max_seqs:
             return False
         return L.decode_layers_workspace_size(len(self.p.layers), B, m.hidden, m.n_heads, m.n_kv_heads, m.head_dim,
                                               m.intermediate, m.tp, self.max_context) > 0
