@@ -139,9 +139,6 @@ __global__ void __launch_bounds__(DK_THREADS, 1) attn_decode_kv8_kernel(const __
   const uint32_t bars = smem_u32(scales + ST * 2 * DK_WARPS);
   auto full = [&](int s) { return bars + 8u * uint32_t(s); };
   auto empty = [&](int s) { return bars + 8u * uint32_t(ST + s); };
-  __shared__ int64_t s_sum[DK_WARPS + 1];
-  __shared__ int64_t s_before;
-  __shared__ int s_first;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < ST; ++s) {
@@ -152,62 +149,57 @@ __global__ void __launch_bounds__(DK_THREADS, 1) attn_decode_kv8_kernel(const __
     tcx::prefetch_map(&tmK);
     tcx::prefetch_map(&tmV);
   }
+  __syncthreads();
   pdl_wait();      // inputs of this kernel are complete and visible
   pdl_trigger();   // only now may the next kernel start its prologue
 
-  // ---- this CTA's share: an equal part of all sequences' visible tiles
+  // ---- this CTA's share: an equal part of all sequences' visible tiles.  Every warp finds it by
+  // itself: a lane takes `chunk` sequences in a row, a scan over the lanes gives the total and
+  // the lane with tile `lo`, which walks through its sequences.
   auto span_of = [&](int b) { return decode_span(a.ctx[b], a.max_ctx, a.window, a.n_sink, KT); };
-  int64_t mine = 0;
-  for (int b = tid; b < a.B; b += DK_THREADS) mine += int64_t(span_of(b).nt) * a.nhg;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) s_sum[warp] = mine;
-  // sequences that see nothing: zero rows (dealt out over the warps of the grid)
-  for (int b = blockIdx.x + gridDim.x * warp; b < a.B; b += gridDim.x * (DK_WARPS + 1)) {
-    const int ctx = a.ctx[b];
-    if (ctx > a.max_ctx && lane == 0) atomicOr(&g_kv8_error, kErrContextOverflow);
-    if (span_of(b).nt == 0)
-      for (int i = lane; i < a.nh * HD / 8; i += 32)
-        *reinterpret_cast<uint4*>(a.out + int64_t(b) * a.nh * HD + 8 * i) = make_uint4(0u, 0u, 0u, 0u);
-  }
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w <= DK_WARPS; ++w) total += s_sum[w];
-  const int64_t per = max(int64_t(DK_MIN_TILES), (total + gridDim.x - 1) / gridDim.x);
-  const int64_t lo = int64_t(blockIdx.x) * per, hi = min(total, lo + per);
-  if (lo >= hi) return;   // uniform over the CTA; no barrier is in use yet
-  if (warp == 0) {        // the sequence that holds tile `lo`: a scan, 32 sequences at a time
-    int64_t before = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-      const int b = b0 + lane;
-      const int64_t n = b < a.B ? int64_t(span_of(b).nt) * a.nhg : 0;
-      int64_t upto = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
-      }
-      const bool here = lo >= before + upto - n && lo < before + upto;
-      if (here) {
-        s_first = b;
-        s_before = before + upto - n;
-      }
-      if (__any_sync(0xffffffffu, here)) break;
-      before += __shfl_sync(0xffffffffu, upto, 31);
+  const int chunk = (a.B + 31) / 32;
+  int mine = 0;
+  for (int i = 0; i < chunk; ++i) {
+    const int b = lane * chunk + i, ctx = b < a.B ? a.ctx[b] : 1;
+    const int nt = b < a.B ? decode_span(ctx, a.max_ctx, a.window, a.n_sink, KT).nt : 0;
+    mine += nt * a.nhg;
+    // of the sequences dealt to this CTA: note a context that is too long, zero the rows of one that sees nothing
+    const bool dealt = warp == 1 && b < a.B && b % gridDim.x == blockIdx.x;
+    if (dealt && ctx > a.max_ctx) atomicOr(&g_kv8_error, kErrContextOverflow);
+    for (unsigned m = __ballot_sync(0xffffffffu, dealt && nt == 0); m; m &= m - 1) {
+      const int64_t zb = int64_t(__ffs(m) - 1) * chunk + i;
+      for (int c = lane; c < a.nh * HD / 8; c += 32)
+        *reinterpret_cast<uint4*>(a.out + zb * a.nh * HD + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
     }
   }
-  __syncthreads();
+  int upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  const int total = __shfl_sync(0xffffffffu, upto, 31);
+  const int per = max(DK_MIN_TILES, (total + int(gridDim.x) - 1) / int(gridDim.x));
+  const int lo = int(blockIdx.x) * per, hi = min(total, lo + per);
+  if (lo >= hi) return;   // uniform over the CTA
   // position in the share: tile t of kv head group hg of sequence b; `start` is the
   // first tile of that (sequence, group) in the common order
-  int b = s_first, hg, t;
-  Span sp = span_of(b);
+  int b = 0, before = upto - mine;
   {
-    const int64_t off = lo - s_before;
-    hg = int(off / sp.nt);
-    t = int(off % sp.nt);
+    const bool here = lo >= before && lo < upto;
+    if (here)
+      for (b = lane * chunk;; ++b) {
+        const int n = span_of(b).nt * a.nhg;
+        if (lo < before + n) break;
+        before += n;
+      }
+    const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+    b = __shfl_sync(0xffffffffu, b, src);
+    before = __shfl_sync(0xffffffffu, before, src);
   }
-  const int count = int(hi - lo);
+  Span sp = span_of(b);
+  int hg = (lo - before) / sp.nt, t = (lo - before) % sp.nt;
+  const int count = hi - lo;
   auto next_pair = [&]() {   // only while a tile is left
     t = 0;
     if (++hg == a.nhg) {
@@ -265,7 +257,7 @@ __global__ void __launch_bounds__(DK_THREADS, 1) attn_decode_kv8_kernel(const __
   // ---------------- consumer warps
   const int gq = lane >> 2, tq = lane & 3;
   const int h = warp % HG, ks = warp / HG;
-  int64_t start = lo - t;
+  int start = lo - t;
   int j = 0;
   while (j < count) {
     if (t == sp.nt) {
@@ -511,7 +503,7 @@ __global__ void __launch_bounds__(DK_THREADS, 1) attn_decode_kv8_kernel(const __
       asm volatile("bar.sync 1, %0;" ::"n"(32 * DK_WARPS) : "memory");   // the area is free again
     }
     if (ks == 0 && head_ok) {
-      const int c_first = int(start / per), c_last = int((start + sp.nt - 1) / per);
+      const int c_first = start / per, c_last = (start + sp.nt - 1) / per;
       const bool split = c_first != c_last;
       const int pair = b * a.nhg + hg;
 #pragma unroll
@@ -638,6 +630,8 @@ int launch_decode(const DecodeArgs& a, int64_t num_slots, cudaStream_t st) {
   int64_t tiles = (int64_t(a.max_ctx) + KT - 1) / KT;
   if (a.window > 0)
     tiles = std::min(tiles, (int64_t(a.window) + KT - 1) / KT + 1 + (int64_t(a.n_sink) + KT - 1) / KT);
+  if (tiles * a.B * a.nhg > INT32_MAX / 2)
+    return set_error(QW_ERR_SHAPE, "qw_attention_decode_kv8: %d sequences of up to %d keys are too many", a.B, a.max_ctx);
   const int64_t ctas = (std::max<int64_t>(tiles, 1) * a.B * a.nhg + DK_MIN_TILES - 1) / DK_MIN_TILES;
   launch_pdl(attn_decode_kv8_kernel<KV, HG, NT>, unsigned(std::min<int64_t>(ctas, DK_CTAS)), DK_THREADS,
              dk_smem<HG, NT>(), st, mk, mv, a);
