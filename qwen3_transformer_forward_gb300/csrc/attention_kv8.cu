@@ -258,6 +258,11 @@ __global__ void __launch_bounds__(DK_THREADS, 1) attn_decode_kv8_kernel(const __
   const int gq = lane >> 2, tq = lane & 3;
   const int h = warp % HG, ks = warp / HG;
   int start = lo - t;
+  // split pairs whose part this warp has written: the first of the share, counted during the
+  // next pair's tiles (so that neither the fence nor the atomic holds up the ring), and the last
+  int pend = 0, p0_b = 0, p0_hg = 0, p0_first = 0, p0_last = 0, p1_b = 0, p1_hg = 0, p1_first = 0, p1_last = 0;
+  bool counted = false;
+  unsigned int done = 0;
   int j = 0;
   while (j < count) {
     if (t == sp.nt) {
@@ -445,6 +450,12 @@ __global__ void __launch_bounds__(DK_THREADS, 1) attn_decode_kv8_kernel(const __
         tcx::mbar_arrive(empty(st[0]));
         if (two) tcx::mbar_arrive(empty(st[UN - 1]));
       }
+      if (pend == 1 && !counted && i >= UN) {   // (the part's stores are a step old: the fence is short)
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) done = atom_add_acq_rel(a.counters + p0_b * a.nkv + p0_hg * HG + h, 1u);
+        counted = true;
+      }
       if (UN > 1 && !two) {   // the part's last tile stood alone
         --j;
         --t;
@@ -531,68 +542,80 @@ __global__ void __launch_bounds__(DK_THREADS, 1) attn_decode_kv8_kernel(const __
             }
           }
         }
-      if (split) {
-        __threadfence();
-        __syncwarp();
-        unsigned int before = 0;
-        if (lane == 0) before = atom_add_acq_rel(a.counters + b * a.nkv + g, 1u);
-        before = __shfl_sync(0xffffffffu, before, 0);
-        if (before == unsigned(c_last - c_first)) {
-          __threadfence();
-          // four heads at a time, four CTAs' parts each: 32 loads in flight for a lane
-          for (int h0 = 0; h0 < a.G; h0 += 4) {
-            auto index = [&](int c, int u) { return ((int64_t(c) + pair) * HG + h) * a.G + min(h0 + u, a.G - 1); };
-            float M[4], lsum[4];
-            float4 acc[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              M[u] = -INFINITY;
-              lsum[u] = 0.0f;
-              acc[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            }
-            for (int c = c_first + lane; c <= c_last; c += 32)
-#pragma unroll
-              for (int u = 0; u < 4; ++u) M[u] = fmaxf(M[u], __ldcg(a.ws_ml + 2 * index(c, u)));
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              M[u] = warp_max(M[u]);
-              if (M[u] == -INFINITY) M[u] = 0.0f;
-            }
-            for (int c0 = c_first; c0 <= c_last; c0 += 4) {
-              float2 ml[4][4];
-              float4 x[4][4];
-#pragma unroll
-              for (int v = 0; v < 4; ++v)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                  const int64_t idx = index(min(c0 + v, c_last), u);
-                  ml[v][u] = __ldcg(reinterpret_cast<const float2*>(a.ws_ml) + idx);
-                  x[v][u] = __ldcg(reinterpret_cast<const float4*>(a.ws_o + idx * HD) + lane);
-                }
-#pragma unroll
-              for (int v = 0; v < 4; ++v)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                  const float w = c0 + v <= c_last ? ex2(ml[v][u].x - M[u]) : 0.0f;
-                  lsum[u] = fmaf(ml[v][u].y, w, lsum[u]);
-                  acc[u].x = fmaf(x[v][u].x, w, acc[u].x);
-                  acc[u].y = fmaf(x[v][u].y, w, acc[u].y);
-                  acc[u].z = fmaf(x[v][u].z, w, acc[u].z);
-                  acc[u].w = fmaf(x[v][u].w, w, acc[u].w);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              if (h0 + u >= a.G) continue;
-              const float fac = lsum[u] > 0.0f ? kUnshift / lsum[u] : 0.0f;
-              *reinterpret_cast<uint2*>(a.out + (int64_t(b) * a.nh + g * a.G + h0 + u) * HD + 4 * lane) =
-                  make_uint2(pack_bf16(acc[u].x * fac, acc[u].y * fac), pack_bf16(acc[u].z * fac, acc[u].w * fac));
-            }
-          }
-          if (lane == 0) a.counters[b * a.nkv + g] = 0u;
+      if (split) {   // the first and the last pair of a share at most
+        if (pend == 0) {
+          p0_b = b; p0_hg = hg; p0_first = c_first; p0_last = c_last;
+        } else {
+          p1_b = b; p1_hg = hg; p1_first = c_first; p1_last = c_last;
         }
+        ++pend;
       }
     }
+  }
+  // ---- pairs that other CTAs work on too: this CTA's part counts as done, and the last to be
+  // done adds the parts
+#pragma unroll 1
+  for (int k = 0; k < pend; ++k) {
+    const int pb = k ? p1_b : p0_b, phg = k ? p1_hg : p0_hg, c_first = k ? p1_first : p0_first, c_last = k ? p1_last : p0_last;
+    const int g = phg * HG + h, pair = pb * a.nhg + phg;
+    if (k || !counted) {
+      __threadfence();
+      __syncwarp();
+      if (lane == 0) done = atom_add_acq_rel(a.counters + pb * a.nkv + g, 1u);
+    }
+    if (__shfl_sync(0xffffffffu, done, 0) != unsigned(c_last - c_first)) continue;
+    __threadfence();
+    // four heads at a time, four CTAs' parts each: 32 loads in flight for a lane
+    for (int h0 = 0; h0 < a.G; h0 += 4) {
+      auto index = [&](int c, int u) { return ((int64_t(c) + pair) * HG + h) * a.G + min(h0 + u, a.G - 1); };
+      float M[4], lsum[4];
+      float4 acc[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        M[u] = -INFINITY;
+        lsum[u] = 0.0f;
+        acc[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+      for (int c = c_first + lane; c <= c_last; c += 32)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) M[u] = fmaxf(M[u], __ldcg(a.ws_ml + 2 * index(c, u)));
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        M[u] = warp_max(M[u]);
+        if (M[u] == -INFINITY) M[u] = 0.0f;
+      }
+      for (int c0 = c_first; c0 <= c_last; c0 += 4) {
+        float2 ml[4][4];
+        float4 x[4][4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int64_t idx = index(min(c0 + v, c_last), u);
+            ml[v][u] = __ldcg(reinterpret_cast<const float2*>(a.ws_ml) + idx);
+            x[v][u] = __ldcg(reinterpret_cast<const float4*>(a.ws_o + idx * HD) + lane);
+          }
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float w = c0 + v <= c_last ? ex2(ml[v][u].x - M[u]) : 0.0f;
+            lsum[u] = fmaf(ml[v][u].y, w, lsum[u]);
+            acc[u].x = fmaf(x[v][u].x, w, acc[u].x);
+            acc[u].y = fmaf(x[v][u].y, w, acc[u].y);
+            acc[u].z = fmaf(x[v][u].z, w, acc[u].z);
+            acc[u].w = fmaf(x[v][u].w, w, acc[u].w);
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (h0 + u >= a.G) continue;
+        const float fac = lsum[u] > 0.0f ? kUnshift / lsum[u] : 0.0f;
+        *reinterpret_cast<uint2*>(a.out + (int64_t(pb) * a.nh + g * a.G + h0 + u) * HD + 4 * lane) =
+            make_uint2(pack_bf16(acc[u].x * fac, acc[u].y * fac), pack_bf16(acc[u].z * fac, acc[u].w * fac));
+      }
+    }
+    if (lane == 0) a.counters[pb * a.nkv + g] = 0u;
   }
 }
 
