@@ -128,8 +128,14 @@ def _dev_ptr(t: Optional[torch.Tensor], name: str):
     return t.data_ptr()
 
 
+# torch.cuda.current_stream() builds a Stream object: 2.9 us of a call of about 10, the raw handle 0.3
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
