@@ -176,3 +176,31 @@ def test_negative_softmax_scale(L):
     r = c.rows(0, 0, 150)
     o, tol = K.attend64(qp.double(), c.values("k", r), c.values("v", r), torch.arange(110, 150), -0.1, 0, 0)
     assert torch.all((outp.cpu().double() - o).abs() <= tol)
+
+
+@pytest.mark.parametrize("kv", [I8, E4])
+@pytest.mark.parametrize("lens,lq,nh,nkv", [([1500, 1100, 1024], [7, 3, 1], 8, 2), ([1025], [16], 8, 1), ([5000, 1], [5, 1], 4, 4),
+                                            ([1300] * 30, [2] * 30, 16, 8), ([9000], [64], 2, 1), ([1200, 900], [65, 12], 2, 1)])
+@pytest.mark.parametrize("window,sink", [(0, 0), (700, 100), (64, 4)])
+def test_prefill_few_rows(L, kv, lens, lq, nh, nkv, window, sink):
+    """Few rows over many keys: the keys are split, and the parts added."""
+    c = Paged(lens, nkv, kv, 32, 128, seed=3)
+    q = torch.randn(sum(lq), nh, HD, generator=gen(4)).bfloat16()
+    out = K._prefill(L, c.cuda(), q.cuda(), lens, lq, nh, window, sink)
+    sync_ok(L)
+    K._check_prefill(out, c, q, lens, lq, window, sink)
+
+
+def test_prefill_few_rows_that_see_nothing(L):
+    """As above, with sequences without keys and queries at negative positions."""
+    lens, lq, nh, nkv = [3, 0, 2000], [6, 4, 5], 4, 2
+    c = Paged(lens, nkv, I8, 16, 64, seed=1)
+    q = torch.randn(sum(lq), nh, HD, generator=gen(5)).bfloat16()
+    out = K._prefill(L, c.cuda(), q.cuda(), lens, lq, nh, 0, 0)
+    sync_ok(L)
+    assert torch.all(out[:3] == 0) and torch.all(out[6:10] == 0)
+    K._check_prefill(out[3:6], c, q[3:6], [3], [3], 0, 0)
+    d = Paged.__new__(Paged)
+    d.__dict__.update(c.__dict__)
+    d.table = c.table[2:]
+    K._check_prefill(out[10:], d, q[10:], [2000], [5], 0, 0)
