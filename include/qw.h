@@ -5,8 +5,8 @@
  * Qwen3 forward pass: the vocab-sharded embedding, fused residual add +
  * RMSNorm, the linear layers (merged QKV and gate_up column splits, o_proj
  * and down_proj row splits), per-head QK-RMSNorm + RoPE + KV-cache store,
- * causal GQA attention for prefill and decode, SiluAndMul and the
- * vocab-sharded lm_head with greedy argmax.
+ * causal GQA attention for prefill and decode (over a bf16 or an 8-bit KV
+ * cache), SiluAndMul and the vocab-sharded lm_head with greedy argmax.
  *
  * Sources, cited by page and section:
  *   [VH]  devpress page "vocab 切 / head 切" (nano-vllm tensor parallelism):
