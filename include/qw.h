@@ -316,7 +316,9 @@ int qw_attention_prefill_paged(const void* q, const void* k_cache, const void* v
  *       sits at key position context_lens[s] - Lq + i.
  * All are bf16 with head_dim 128.  Errors: QW_ERR_DTYPE (dtype, kv_dtype),
  * QW_ERR_SHAPE (head_dim, heads, scale_block, block_size, num_slots,
- * max_context), QW_ERR_INVALID_ARG (null or misaligned pointers, negative
+ * max_context; append: T * (nh + 2 nkv) over 2^30; decode: B * nkv over 16384,
+ * or more than 2^30 key tiles; prefill: over 65535 sequences or kv heads),
+ * QW_ERR_INVALID_ARG (null or misaligned pointers, negative
  * sizes), QW_ERR_WORKSPACE.
  *
  * qw_kv8_append: qw_qkv_norm_rope_store_kv into this cache: per-head
@@ -365,8 +367,8 @@ int qw_kv8_read(const void* k_cache, const void* v_cache, const float* k_scale, 
  * j > p - window or j < n_sink; window 0 means every key j <= p.  A query that
  * sees no key gets a zero row.  nh / nkv from 1 to 16, any whole number.
  *   q, out bf16 [tokens, nh, 128], 16-byte aligned; scale: the softmax scale.
- *   max_context >= every context_lens[s], at most max_blocks * block_size (it
- *   sizes the split of the keys; a larger entry is recorded for
+ *   max_context >= every context_lens[s], at most max_blocks * block_size and
+ *   2^30 (it sizes the split of the keys; a larger entry is recorded for
  *   qw_device_error, and the keys from max_context on are not read).
  *   workspace: *_workspace_size bytes, 16-byte aligned, zero-filled when
  *   allocated; may be NULL only when that size is 0.  Prefill leaves the first

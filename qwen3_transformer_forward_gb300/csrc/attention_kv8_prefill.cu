@@ -702,6 +702,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
 }
 
 // Adds the splits' parts in order: one warp per packed row, lane owns dims 4 lane .. + 3.
+// At most 152 x 256 rows of parts, 20 MB, which L2 still holds: bound by latency.
 __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs a) {
   pdl_wait();      // inputs of this kernel are complete and visible
   pdl_trigger();   // only now may the next kernel start its prologue
@@ -822,8 +823,8 @@ extern "C" int qw_attention_prefill_kv8(const void* q, const void* k_cache, cons
   a.nh = n_heads;
   a.nkv = n_kv_heads;
   a.G = n_heads / n_kv_heads;
-  a.window = window;
-  a.n_sink = n_sink;
+  a.window = std::min(window, kv8::kMaxPositions);
+  a.n_sink = std::min(n_sink, max_context);
   a.splits = kv8p::prefill_splits(n_seqs, max_seqlen_q, max_context, n_heads, n_kv_heads);
   a.scale_log2 = fabsf(scale) * kv8p::kLog2e;
   a.q_sign = scale < 0.0f ? -1.0f : 1.0f;

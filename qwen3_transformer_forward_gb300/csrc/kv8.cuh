@@ -17,6 +17,8 @@ namespace qw {
 namespace kv8 {
 
 constexpr int HD = 128;
+// Key positions of a sequence end below this, so that p - window and a tile's last key stay in 32 bits.
+constexpr int kMaxPositions = 1 << 30;
 // A block scale below this is stored as zero with zero codes: 1 / scale stays
 // finite, and the attention kernels' logarithm of a scale stays in range.
 constexpr float kTinyScale = 7.888609052210118e-31f;   // 2^-100
@@ -102,12 +104,12 @@ inline int check_cache(const char* who, const void* k, const void* v, const floa
     return set_error(QW_ERR_INVALID_ARG, "%s: scales must be 4-byte aligned", who);
   return QW_OK;
 }
-inline int check_table(const char* who, const int32_t* table, int max_blocks, int block_size, int scale_block) {
+// (scale_block, 16, 32 or 64, divides block_size)
+inline int check_table(const char* who, const int32_t* table, int max_blocks, int block_size) {
   if (!table) return set_error(QW_ERR_INVALID_ARG, "%s: null block table", who);
   if (max_blocks <= 0 || block_size <= 0 || block_size % 64)
     return set_error(QW_ERR_SHAPE, "%s: block_size %d must be a positive multiple of 64, max_blocks positive", who,
                      block_size);
-  (void)scale_block;   // 16, 32 or 64: divides block_size
   return QW_OK;
 }
 

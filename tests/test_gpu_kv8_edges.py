@@ -204,3 +204,79 @@ def test_prefill_few_rows_that_see_nothing(L):
     d.__dict__.update(c.__dict__)
     d.table = c.table[2:]
     K._check_prefill(out[10:], d, q[10:], [2000], [5], 0, 0)
+
+
+BIG = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("lens,lq", [([40, 300, 5], [200, 300, 9]), ([2000, 3], [12, 30])])
+def test_largest_window_and_sink(L, lens, lq):
+    """The largest window sees every key, and so does any window whose first tokens are all of them,
+    also for queries at negative positions (which see nothing)."""
+    nh, nkv = 8, 2
+    c = Paged(lens, nkv, I8, 16, 64, seed=8)
+    d = c.cuda()
+    q = torch.randn(sum(lq), nh, HD, generator=gen(3)).bfloat16().cuda()
+    qd = torch.randn(len(lens), nh, HD, generator=gen(4)).bfloat16().cuda()
+    want, wantd = K._prefill(L, d, q, lens, lq, nh, 0, 0), K._decode(L, d, qd, lens, nh, 0, 0)
+    sync_ok(L)
+    K._check_decode(wantd, c, qd.cpu(), lens, 0, 0)
+    at = 0
+    for n, m in zip(lens, lq):
+        assert torch.all(want[at:at + max(m - n, 0)] == 0)
+        at += m
+    for window, sink in ((BIG, 0), (BIG, BIG), (BIG - 1, 7), (1 << 30, 0)):
+        assert torch.equal(K._prefill(L, d, q, lens, lq, nh, window, sink), want)
+        assert torch.equal(K._decode(L, d, qd, lens, nh, window, sink), wantd)
+    for window in (1, 70):   # (the tiles are dealt out in another order of sums)
+        sink = K._decode(L, d, qd, lens, nh, window, BIG)
+        K._check_decode(sink, c, qd.cpu(), lens, 0, 0)
+        out = K._prefill(L, d, q, lens, lq, nh, window, BIG).cpu()
+        at = 0
+        for s, (n, m) in enumerate(zip(lens, lq)):
+            skip = max(m - n, 0)
+            assert torch.all(out[at:at + skip] == 0)
+            one = K._only(c, s)
+            K._check_prefill(out[at + skip:at + m], one, q[at + skip:at + m].cpu(), [n], [m - skip], 0, 0)
+            at += m
+    sync_ok(L)
+
+
+def test_no_context_at_all(L):
+    """max_context 0: every sequence is empty, every row zero."""
+    nh, nkv, lens = 4, 2, [0, 0, 0]
+    d = Paged(lens, nkv, E4, 16, 64, seed=8).cuda()
+    q = torch.randn(3, nh, HD, generator=gen(3)).bfloat16().cuda()
+    assert torch.all(K._decode(L, d, q, lens, nh, 0, 0) == 0)
+    assert torch.all(K._prefill(L, d, q, lens, [1, 1, 1], nh, 0, 0) == 0)
+    sync_ok(L)
+
+
+def test_sequences_share_a_prefix(L):
+    """Two sequences whose first pages are the same pages of the cache, each with its own last page."""
+    nh, nkv, lens, lq = 8, 2, [200, 170, 190], [72, 42, 62]
+    c = Paged(lens, nkv, I8, 16, 64, seed=9)
+    c.table[1:, :2] = c.table[0, :2]
+    q = torch.randn(3, nh, HD, generator=gen(3)).bfloat16()
+    qp = torch.randn(sum(lq), nh, HD, generator=gen(4)).bfloat16()
+    d = c.cuda()
+    out, outp = K._decode(L, d, q.cuda(), lens, nh, 0, 0), K._prefill(L, d, qp.cuda(), lens, lq, nh, 0, 0)
+    sync_ok(L)
+    K._check_decode(out, c, q, lens, 0, 0)
+    K._check_prefill(outp, c, qp, lens, lq, 0, 0)
+
+
+def test_append_one_token_with_and_without_offsets(L):
+    """Offsets of one token a sequence and none at all are the same call."""
+    nh, nkv, lens = 8, 2, [70, 1, 64, 65, 33]
+    qkv, qg, kg, pos = K._append_case(nh, nkv, 1, lens, [1] * 5, 8)
+    cs = L.rope_cos_sin_table(80, HD, 1e6).cuda()
+    got = []
+    for cu in (None, torch.arange(6, dtype=torch.int32).cuda()):
+        d = Paged(lens, nkv, I8, 32, 64, seed=3).cuda()
+        q = torch.empty(5, nh, HD, dtype=torch.bfloat16, device="cuda")
+        L.kv8_append(qkv.cuda(), nh, nkv, HD, 1, pos.cuda(), cs, qg.cuda(), kg.cuda(), 1e-6, cu,
+                     torch.tensor(lens, dtype=torch.int32).cuda(), d.table, 64, d.k, d.v, d.ks, d.vs, 32, q)
+        sync_ok(L)
+        got.append([q] + [t.view(torch.uint8) for t in (d.k, d.v, d.ks, d.vs)])
+    assert all(torch.equal(a, b) for a, b in zip(*got))

@@ -100,6 +100,10 @@ def test_workspace_refusals(lib):
             assert _call(lib, "qw_attention_prefill_kv8", list(PREFILL), PREFILL, **args, **kw) == WS
     # more (sequence, kv head) pairs than completion counters
     assert _call(lib, "qw_attention_decode_kv8", list(DECODE), DECODE, n=20000) == SHAPE
+    # sizes past the 32-bit counts of a call
+    assert _call(lib, "qw_attention_decode_kv8", list(DECODE), DECODE, n=2048, maxb=1 << 18, bs=64, mc=1 << 24) == SHAPE
+    assert _call(lib, "qw_kv8_append", list(APPEND), APPEND, T=1 << 28) == SHAPE
+    assert _call(lib, "qw_attention_prefill_kv8", list(PREFILL), PREFILL, n=70000) == SHAPE
     # sizes that no call takes have no workspace
     for bad in ((-1, 64, 16, 8), (2, -1, 16, 8), (2, 64, 0, 8), (2, 64, 16, 0)):
         assert lib.qw_attention_decode_kv8_workspace_size(*bad) == 0
@@ -125,3 +129,10 @@ def test_binding_checks_types_and_sizes(lib):
         with pytest.raises(L.QwError) as err:
             L.kv_code(*args)
         assert err.value.code == SHAPE
+
+
+def test_positions_end_at_2_to_30(lib):
+    for op in ("decode", "prefill"):
+        name, base = ENTRY[op]
+        for mc, want in (((1 << 30) + 1, SHAPE), (1 << 30, OK)):
+            assert _call(lib, name, list(base), base, n=0, maxb=1 << 25, bs=64, mc=mc) == want
