@@ -131,6 +131,53 @@ def test_binding_checks_types_and_sizes(lib):
         assert err.value.code == SHAPE
 
 
+def test_binding_refuses_what_the_library_cannot_see(lib, monkeypatch):
+    """Head counts against the cache's shape, index types, sequence counts, output types and sizes."""
+    monkeypatch.setattr(L, "_dev_ptr", lambda t, name: None if t is None else 64)
+    monkeypatch.setattr(L, "_stream", lambda s: None)
+    i32 = lambda *n: torch.zeros(*n, dtype=torch.int32)
+    bf = lambda *n: torch.zeros(*n, dtype=torch.bfloat16)
+    k, sc = torch.zeros(128, 2, 128, dtype=torch.int8), torch.zeros(2, 2)
+    rows = torch.zeros(3, dtype=torch.int64)
+    base = dict(qkv=bf(0, 8 * 128), nh=4, nkv=2, pos=rows, cs=torch.zeros(64, 128), qg=bf(128), kg=bf(128), cu=i32(4), ctx=i32(3),
+                table=i32(3, 2), q_out=bf(0, 4, 128), q=bf(0, 4, 128), out=bf(0, 4, 128), rows=rows[:0], k_out=None, v_out=None)
+
+    def append(a):
+        L.kv8_append(a["qkv"], a["nh"], a["nkv"], 128, 1, a["pos"], a["cs"], a["qg"], a["kg"], 1e-6, a["cu"], a["ctx"], a["table"],
+                     64, k, k, sc, sc, 64, a["q_out"])
+
+    def read(a):
+        L.kv8_read(k, k, sc, sc, 64, a["rows"], a["k_out"], a["v_out"])
+
+    def decode(a):
+        L.attention_decode_kv8(a["q"], k, k, sc, sc, 64, a["ctx"], a["table"], 64, 128, a["nh"], a["nkv"], 128, 0.1, a["out"], None)
+
+    def prefill(a):
+        L.attention_prefill_kv8(a["q"], k, k, sc, sc, 64, a["cu"], a["ctx"], a["table"], 64, 4, 128, a["nh"], a["nkv"], 128, 0.1,
+                                a["out"], None)
+
+    for f in (append, read, decode, prefill):
+        f(base)   # no tokens, no rows: nothing to do
+    both = (append, prefill)
+    for fs, kw, want in (
+            ((append, decode, prefill), dict(nh=2, nkv=1), SHAPE), ((append, decode, prefill), dict(ctx=rows), DT),
+            ((append, decode, prefill), dict(table=torch.zeros(3, 2, dtype=torch.int64)), DT), (both, dict(cu=rows), DT),
+            (both, dict(table=i32(2, 2)), SHAPE), (both, dict(ctx=i32(2)), SHAPE), ((decode,), dict(q=bf(4, 4, 128)), SHAPE),
+            ((decode, prefill), dict(out=torch.zeros(0, 4, 128)), DT),
+            ((decode, prefill), dict(q=bf(2, 4, 128), out=bf(1, 4, 128)), SHAPE),
+            ((decode, prefill), dict(q=bf(1, 3, 128), out=bf(1, 4, 128)), SHAPE),
+            ((append,), dict(qkv=bf(2, 8 * 128)), SHAPE), ((append,), dict(qkv=bf(2, 6 * 128), q_out=bf(2, 4, 128)), SHAPE),
+            ((append,), dict(qkv=bf(4, 8 * 128), q_out=bf(4, 4, 128)), SHAPE), ((append,), dict(cs=torch.zeros(64, 64)), SHAPE),
+            ((append,), dict(pos=i32(3)), DT), ((append,), dict(cs=bf(64, 128)), DT), ((append,), dict(kg=torch.zeros(128)), DT),
+            ((read,), dict(rows=i32(3), k_out=bf(3, 2, 128)), DT), ((read,), dict(rows=rows, k_out=bf(2, 2, 128)), SHAPE),
+            ((read,), dict(rows=rows, v_out=bf(2, 2, 128)), SHAPE),
+            ((read,), dict(rows=rows, k_out=torch.zeros(3, 2, 128), v_out=bf(3, 2, 128)), DT)):
+        for f in fs:
+            with pytest.raises(L.QwError) as err:
+                f(dict(base, **kw))
+            assert err.value.code == want, (f.__name__, kw)
+
+
 def test_positions_end_at_2_to_30(lib):
     for op in ("decode", "prefill"):
         name, base = ENTRY[op]
