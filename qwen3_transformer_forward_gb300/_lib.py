@@ -289,10 +289,11 @@ _KV_CODES = {torch.int8: QW_I8, torch.float8_e4m3fn: QW_E4M3}
 def kv_code(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
             scale_block: int) -> int:
     """kv_dtype of an 8-bit cache; the library sees pointers only, so the tensors' types and sizes are checked here."""
-    code = _KV_CODES.get(k_cache.dtype)
-    if code is None or v_cache.dtype != k_cache.dtype:
+    kind = k_cache.dtype
+    code = _KV_CODES.get(kind)
+    if code is None or v_cache.dtype is not kind:
         raise QwError(QW_ERR_DTYPE, f"caches must both be int8 or float8_e4m3fn, not {k_cache.dtype} and {v_cache.dtype}")
-    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+    if k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32:
         raise QwError(QW_ERR_DTYPE, "scales must be float32")
     shape = k_cache.shape
     want = (shape[0] // scale_block if scale_block > 0 else -1, shape[1])
@@ -302,22 +303,27 @@ def kv_code(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
     return code
 
 
-def _kv8_check(k_cache, n_kv_heads, head_dim, n_seqs, context_lens, block_table, cu_seqlens_q, x, y, x_heads, y_heads):
+def _kv8_check(k_cache, n_kv_heads, head_dim, n_seqs, context_lens, block_table, x, y, x_heads, y_heads):
     """Types and sizes of a call on the 8-bit cache: x (tokens of x_heads heads) goes in, y (y_heads) comes out."""
-    if tuple(k_cache.shape[1:]) != (n_kv_heads, head_dim):
-        raise QwError(QW_ERR_SHAPE, f"the cache holds {tuple(k_cache.shape[1:])} per token, not {(n_kv_heads, head_dim)}")
-    for t in (context_lens, block_table) if cu_seqlens_q is None else (context_lens, block_table, cu_seqlens_q):
-        if t.dtype != torch.int32:
-            raise QwError(QW_ERR_DTYPE, f"context_lens, block_table and cu_seqlens_q must be int32, not {t.dtype}")
-    if context_lens.numel() < n_seqs or block_table.shape[0] < n_seqs:
-        raise QwError(QW_ERR_SHAPE, f"{context_lens.numel()} context_lens and {block_table.shape[0]} block table rows for "
-                                    f"{n_seqs} sequences")
-    if y.dtype != x.dtype:
-        raise QwError(QW_ERR_DTYPE, f"the output's type {y.dtype} is not the input's, {x.dtype}")
-    tokens = x.shape[0]
-    if x.numel() != tokens * x_heads * head_dim or y.numel() < tokens * y_heads * head_dim:
+    _, nkv, hd = k_cache.shape
+    if nkv != n_kv_heads or hd != head_dim:
+        raise QwError(QW_ERR_SHAPE, f"the cache holds {(nkv, hd)} per token, not {(n_kv_heads, head_dim)}")
+    if context_lens.dtype is not torch.int32 or block_table.dtype is not torch.int32:
+        raise QwError(QW_ERR_DTYPE, f"context_lens and block_table must be int32, not {context_lens.dtype}, {block_table.dtype}")
+    rows, tokens, dtype = block_table.shape[0], x.shape[0], x.dtype
+    if context_lens.numel() < n_seqs or rows < n_seqs:
+        raise QwError(QW_ERR_SHAPE, f"{context_lens.numel()} context_lens and {rows} block table rows for {n_seqs} sequences")
+    if y.dtype is not dtype:
+        raise QwError(QW_ERR_DTYPE, f"the output's type {y.dtype} is not the input's, {dtype}")
+    if x.numel() != tokens * x_heads * hd or y.numel() < tokens * y_heads * hd:
         raise QwError(QW_ERR_SHAPE, f"{tuple(x.shape)} in and {tuple(y.shape)} out are not {tokens} tokens of {x_heads} and "
                                     f"{y_heads} heads")
+
+
+def _kv8_seqs(cu_seqlens_q) -> int:
+    if cu_seqlens_q.dtype is not torch.int32:
+        raise QwError(QW_ERR_DTYPE, f"cu_seqlens_q must be int32, not {cu_seqlens_q.dtype}")
+    return cu_seqlens_q.shape[0] - 1
 
 
 def kv8_append(qkv, n_heads, n_kv_heads, head_dim, tp, positions, cos_sin, q_gamma, k_gamma, eps, cu_seqlens_q,
@@ -325,9 +331,9 @@ def kv8_append(qkv, n_heads, n_kv_heads, head_dim, tp, positions, cos_sin, q_gam
                err_count=None, stream=None):
     """QK-norm + RoPE, q out, k and v quantised into an 8-bit paged cache; cu_seqlens_q None: one token per sequence."""
     kv = kv_code(k_cache, v_cache, k_scale, v_scale, scale_block)
-    n_seqs = context_lens.shape[0] if cu_seqlens_q is None else cu_seqlens_q.shape[0] - 1
-    _kv8_check(k_cache, n_kv_heads, head_dim, n_seqs, context_lens, block_table, cu_seqlens_q, qkv, q_out,
-               n_heads + 2 * n_kv_heads, n_heads)
+    n_seqs = context_lens.shape[0] if cu_seqlens_q is None else _kv8_seqs(cu_seqlens_q)
+    _kv8_check(k_cache, n_kv_heads, head_dim, n_seqs, context_lens, block_table, qkv, q_out, n_heads + 2 * n_kv_heads,
+               n_heads)
     if positions.dtype != torch.int64 or cos_sin.dtype != torch.float32 or q_gamma.dtype != qkv.dtype or k_gamma.dtype != qkv.dtype:
         raise QwError(QW_ERR_DTYPE, "positions must be int64, cos_sin float32, gammas of qkv's type")
     if positions.numel() < qkv.shape[0] or cos_sin.numel() != cos_sin.shape[0] * head_dim:
@@ -345,16 +351,18 @@ def kv8_append(qkv, n_heads, n_kv_heads, head_dim, tp, positions, cos_sin, q_gam
 def kv8_read(k_cache, v_cache, k_scale, v_scale, scale_block, rows, k_out, v_out, err_count=None, stream=None):
     """Values of the 8-bit cache's rows (int64 [n]); k_out or v_out may be None."""
     kv = kv_code(k_cache, v_cache, k_scale, v_scale, scale_block)
-    out = k_out if k_out is not None else v_out
-    if rows.dtype != torch.int64 or (v_out is not None and v_out.dtype != out.dtype):
+    n_slots, nkv, hd = k_cache.shape
+    n, out = rows.shape[0], k_out if k_out is not None else v_out
+    if rows.dtype is not torch.int64 or (v_out is not None and v_out.dtype is not out.dtype):
         raise QwError(QW_ERR_DTYPE, "rows must be int64, k_out and v_out of one type")
-    if any(o is not None and o.numel() < rows.numel() * k_cache.shape[1] * k_cache.shape[2] for o in (k_out, v_out)):
-        raise QwError(QW_ERR_SHAPE, f"outputs are smaller than {rows.numel()} rows of {tuple(k_cache.shape[1:])}")
+    need = n * nkv * hd
+    if (k_out is not None and k_out.numel() < need) or (v_out is not None and v_out.numel() < need):
+        raise QwError(QW_ERR_SHAPE, f"outputs are smaller than {n} rows of {(nkv, hd)}")
     _check(load().qw_kv8_read(
         _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), _dev_ptr(k_scale, "k_scale"),
-        _dev_ptr(v_scale, "v_scale"), k_cache.shape[0], scale_block, k_cache.shape[1], k_cache.shape[2],
-        _dev_ptr(rows, "rows"), rows.shape[0], _dev_ptr(k_out, "k_out"), _dev_ptr(v_out, "v_out"),
-        _dev_ptr(err_count, "err_count"), dtype_code(out.dtype) if out is not None else QW_BF16, kv, _stream(stream)))
+        _dev_ptr(v_scale, "v_scale"), n_slots, scale_block, nkv, hd, _dev_ptr(rows, "rows"), n, _dev_ptr(k_out, "k_out"),
+        _dev_ptr(v_out, "v_out"), _dev_ptr(err_count, "err_count"), dtype_code(out.dtype) if out is not None else QW_BF16, kv,
+        _stream(stream)))
 
 
 def attention_decode_kv8_workspace_size(B, max_context, n_heads, n_kv_heads) -> int:
@@ -366,7 +374,7 @@ def attention_decode_kv8(q, k_cache, v_cache, k_scale, v_scale, scale_block, con
                          stream=None):
     """Decode attention over an 8-bit paged cache; window > 0: the last `window` keys and the first n_sink are seen."""
     kv = kv_code(k_cache, v_cache, k_scale, v_scale, scale_block)
-    _kv8_check(k_cache, n_kv_heads, head_dim, q.shape[0], context_lens, block_table, None, q, out, n_heads, n_heads)
+    _kv8_check(k_cache, n_kv_heads, head_dim, q.shape[0], context_lens, block_table, q, out, n_heads, n_heads)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(load().qw_attention_decode_kv8(
         _dev_ptr(q, "q"), _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), _dev_ptr(k_scale, "k_scale"),
@@ -389,8 +397,8 @@ def attention_prefill_kv8(q, k_cache, v_cache, k_scale, v_scale, scale_block, cu
                           window=0, n_sink=0, stream=None):
     """Causal attention of packed new tokens over an 8-bit paged cache that holds their k and v already."""
     kv = kv_code(k_cache, v_cache, k_scale, v_scale, scale_block)
-    n_seqs = cu_seqlens_q.shape[0] - 1
-    _kv8_check(k_cache, n_kv_heads, head_dim, n_seqs, context_lens, block_table, cu_seqlens_q, q, out, n_heads, n_heads)
+    n_seqs = _kv8_seqs(cu_seqlens_q)
+    _kv8_check(k_cache, n_kv_heads, head_dim, n_seqs, context_lens, block_table, q, out, n_heads, n_heads)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(load().qw_attention_prefill_kv8(
         _dev_ptr(q, "q"), _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), _dev_ptr(k_scale, "k_scale"),
