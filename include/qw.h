@@ -365,7 +365,8 @@ int qw_kv8_read(const void* k_cache, const void* v_cache, const float* k_scale, 
  * Attention over the 8-bit cache, with a sliding window and first tokens that
  * stay visible: the query at key position p sees the keys j <= p with
  * j > p - window or j < n_sink; window 0 means every key j <= p.  A query that
- * sees no key gets a zero row.  nh / nkv from 1 to 16, any whole number.
+ * sees no key gets a zero row, one with NaN that sees a key a row of NaN.
+ * nh / nkv from 1 to 16, any whole number.
  *   q, out bf16 [tokens, nh, 128], 16-byte aligned; scale: the softmax scale.
  *   max_context >= every context_lens[s], at most max_blocks * block_size and
  *   2^30 (it sizes the split of the keys; a larger entry is recorded for

@@ -529,7 +529,8 @@ __global__ void __launch_bounds__(DK_THREADS, 1) attn_decode_kv8_kernel(const __
           const int hd = 8 * n + 2 * tq + e;
           if (hd >= a.G) continue;
           float f[16];
-          const float fac = split ? 1.0f : (l[n][e] > 0.0f ? kUnshift / l[n][e] : 0.0f);
+          // no visible key: l = 0, a zero row; a query with NaN: l NaN, and so is the row
+          const float fac = split ? 1.0f : (l[n][e] == 0.0f ? 0.0f : kUnshift / l[n][e]);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             f[2 * i] = o[n][i][e] * fac;
@@ -615,7 +616,7 @@ __global__ void __launch_bounds__(DK_THREADS, 1) attn_decode_kv8_kernel(const __
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         if (h0 + u >= a.G) continue;
-        const float fac = lsum[u] > 0.0f ? kUnshift / lsum[u] : 0.0f;
+        const float fac = lsum[u] == 0.0f ? 0.0f : kUnshift / lsum[u];   // (NaN stays)
         *reinterpret_cast<uint2*>(a.out + (int64_t(pb) * a.nh + g * a.G + h0 + u) * HD + 4 * lane) =
             make_uint2(pack_bf16(acc[u].x * fac, acc[u].y * fac), pack_bf16(acc[u].z * fac, acc[u].w * fac));
       }

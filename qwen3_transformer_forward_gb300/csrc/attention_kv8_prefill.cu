@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
       tcx::tc_fence_after();
       if (a.splits == 1) {
         // O / l -> bf16, staged in Q_u (every S_u MMA completed before the last PV_u), stored coalesced
-        const float inv = l > 0.0f ? kUnshift / l : 0.0f;
+        const float inv = l == 0.0f ? 0.0f : kUnshift / l;   // no visible key: a zero row; l NaN stays
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t o[32];
@@ -714,6 +714,8 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs a)
   float2 mine = make_float2(-INFINITY, 0.0f);   // part `lane` (at most 32)
   if (lane < a.splits) mine = ml[lane * n + id];
   const float M = warp_max(mine.x);
+  // A part without a visible key has (-inf, 0).  One of a query with NaN may have (-inf, NaN): its
+  // weight is 0 too, but the NaN reaches l, and through l the row.
   const float w = mine.x == -INFINITY ? 0.0f : ex2(mine.x - M);
   const float l = warp_sum(mine.y * w);
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -727,7 +729,7 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs a)
     acc.z = fmaf(x.z, wi, acc.z);
     acc.w = fmaf(x.w, wi, acc.w);
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   *reinterpret_cast<uint2*>(a.out + id * HD + 4 * lane) =
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
