@@ -50,6 +50,9 @@ namespace kv8p {
 using namespace kv8;
 
 __device__ unsigned int g_kv8_prefill_error = 0;
+// A wait that gives up sets bit `code` of the word, 0 .. 15: none is the bit of an overlong context.
+constexpr uint32_t kWaitCodeMask = 15u;
+static_assert((kErrContextOverflow & 0xffffu) == 0u, "the low 16 bits are the waits'");
 
 constexpr int BM = 128, BN = 128, HALF = 64, ROWS = 2 * BM, THREADS = 512;
 constexpr uint32_t BOX = 16384;                    // 128 rows x 64 f16
@@ -385,7 +388,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
   auto wait = [&](int b, uint32_t parity, uint32_t code) {
-    if (ok && !tcx::mbar_wait(bar(b), parity, &g_kv8_prefill_error, 1u << code)) ok = false;
+    if (ok && !tcx::mbar_wait(bar(b), parity, &g_kv8_prefill_error, 1u << (code & kWaitCodeMask))) ok = false;
   };
 
   if (warp < 4) {

@@ -17,8 +17,9 @@ constexpr size_t kCounterBytes = 64 * 1024;
 
 // Bit of the decode-attention error word set when a context_lens entry exceeds
 // the max_context a call was planned for: keys past it are not read, so the
-// output misses them.  qw_device_error reports it as QW_ERR_INVALID_ARG.
-constexpr unsigned int kErrContextOverflow = 0x100u;
+// output misses them.  qw_device_error reports it as QW_ERR_INVALID_ARG.  The
+// low bits of the word belong to the kernels' bounded waits.
+constexpr unsigned int kErrContextOverflow = 1u << 31;
 
 // ---------------------------------------------------------------------------
 // element conversions
