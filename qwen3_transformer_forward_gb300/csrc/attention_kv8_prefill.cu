@@ -36,7 +36,7 @@
 // 8 x 2048 tokens, 16 q / 8 kv heads, int8: 215 us, 640 TFLOP/s; 2 x 2500 new tokens
 // over 24000, 32 / 8 heads, e4m3, window 8192: 639 us, 960 TFLOP/s.
 // Every mbarrier wait is bounded (2 s); on timeout the kernel records an error
-// word and runs to its end without waiting further.
+// word and runs to its end without waiting further, except for its own MMAs in flight.
 #include <math.h>
 
 #include <algorithm>
@@ -450,8 +450,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
           }
         if (t & 1) commit(lead, bar(B_K_EMPTY + (((t + 2) >> 1) & 1)));
       }
-      // every MMA of this CTA has completed before TMEM is released
+      // every MMA of this CTA has completed before TMEM and shared memory are released: waited for
+      // (as long as any wait) after a wait that gave up, too
       commit(lead, bar(B_DONE));
+      ok = true;
       wait(B_DONE, 0u, 11u);
     }
     __syncwarp();
