@@ -387,11 +387,16 @@ class Qwen3Forward:
         with self._around(f"{ph}.gemm_down", l):
             L.gemm(act, p.down, h, m.hidden, tp, L.QW_GEMM_ROW_REDUCE, L.QW_EPI_NONE, self.workspace, stream)
 
+    def _check_kv8(self, ctx, decode: bool):
+        """Refuses a context without the fields that the 8-bit paged cache is addressed by."""
+        if ctx.block_table is None or ctx.context_lens is None:
+            raise ValueError("the 8-bit KV cache needs a context with block_table and context_lens")
+        if not decode and ctx.n_tokens > 0 and ctx.max_context <= 0:   # no key would be read
+            raise ValueError(f"the 8-bit KV cache needs a context with max_context >= every context_lens, not {ctx.max_context}")
+
     def _attention_kv8(self, l: int, qkv, q, attn, ctx, decode: bool, ph: str, stream=None):
         """QK-norm + RoPE + quantised append, then attention over the 8-bit paged cache."""
         m, p, c = self.m, self.p.layers[l], self.kv8
-        if ctx.block_table is None or ctx.context_lens is None:
-            raise ValueError("the 8-bit KV cache needs a context with block_table and context_lens")
         cache = (self.k_cache[l], self.v_cache[l], self.k_scale[l], self.v_scale[l], c.scale_block)
         cu = None if decode else ctx.cu_seqlens
         with self._around(f"{ph}.kv8_append", l):
@@ -447,6 +452,8 @@ class Qwen3Forward:
         """embedding (or hidden_in) -> layers -> optional final add+RMSNorm; returns the hidden buffer view."""
         m = self.m
         T = ctx.n_tokens
+        if self.kv8 is not None:
+            self._check_kv8(ctx, decode)
         if decode and hidden_in is None and final_norm and self.fused_decode_ok(T):
             return self._decode_fused(ctx, stream)
         if hidden_in is None:
