@@ -143,14 +143,22 @@ class DecodeContext:
         return self.ids.shape[0]
 
 
-def to_device_prefill(b, device="cuda") -> PrefillContext:
-    return PrefillContext(b.ids.to(device), b.positions.to(device), b.cu_seqlens.to(device),
-                          b.slot_mapping.to(device), b.seq_base.to(device), b.last_idx.to(device), max(b.seq_lens))
+def to_device_prefill(b, device="cuda", block_table=None, context_lens=None) -> PrefillContext:
+    """block_table (8-bit paged cache): the prompts are whole, or context_lens counts the cached keys before them too."""
+    ctx = PrefillContext(b.ids.to(device), b.positions.to(device), b.cu_seqlens.to(device),
+                         b.slot_mapping.to(device), b.seq_base.to(device), b.last_idx.to(device), max(b.seq_lens))
+    if block_table is not None:
+        lens = torch.tensor(b.seq_lens, dtype=torch.int32) if context_lens is None else context_lens
+        ctx.block_table, ctx.context_lens = block_table.to(device), lens.to(device)
+        ctx.max_context = int(lens.max())
+    return ctx
 
 
-def to_device_decode(b, device="cuda") -> DecodeContext:
+def to_device_decode(b, device="cuda", block_table=None) -> DecodeContext:
+    """block_table: for the 8-bit paged cache."""
     return DecodeContext(b.ids.to(device), b.positions.to(device), b.context_lens.to(device),
-                         b.slot_mapping.to(device), b.seq_base.to(device), int(b.context_lens.max()))
+                         b.slot_mapping.to(device), b.seq_base.to(device), int(b.context_lens.max()),
+                         None if block_table is None else block_table.to(device))
 
 
 # ----------------------------------------------------------------------------

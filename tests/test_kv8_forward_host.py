@@ -1,5 +1,6 @@
 """Host side of the forward pass with an 8-bit KV cache: contexts that cannot be
-answered are refused before any launch."""
+answered are refused before any launch, and the batch descriptions fill in the
+fields that such a model reads."""
 from contextlib import nullcontext
 from types import SimpleNamespace
 
@@ -59,3 +60,20 @@ def test_a_prefill_context_left_at_its_default_is_refused(fwd):
     with pytest.raises(ValueError, match="max_context"):
         fwd.prefill(pre)
     assert not fwd.calls
+
+
+def test_batches_with_a_block_table():
+    """Whole prompts: the cached keys are the prompts themselves; over a cached prefix the caller says how many."""
+    m = si.QWEN3_0_6B
+    b = si.prefill_batch(m, [7, 2, 30])
+    table = torch.arange(6, dtype=torch.int32).view(3, 2)
+    c = M.to_device_prefill(b, "cpu", block_table=table)
+    assert c.block_table is table or torch.equal(c.block_table, table)
+    assert c.context_lens.dtype == torch.int32 and c.context_lens.tolist() == [7, 2, 30] and c.max_context == 30
+    c = M.to_device_prefill(b, "cpu", block_table=table, context_lens=torch.tensor([70, 2, 31], dtype=torch.int32))
+    assert c.context_lens.tolist() == [70, 2, 31] and c.max_context == 70
+    c = M.to_device_prefill(b, "cpu")
+    assert c.block_table is None and c.context_lens is None
+    d = M.to_device_decode(si.decode_batch(m, [5, 9, 3]), "cpu", block_table=table)
+    assert torch.equal(d.block_table, table) and d.max_context == 9
+    assert M.to_device_decode(si.decode_batch(m, [5, 9]), "cpu").block_table is None
