@@ -320,6 +320,15 @@ def _kv8_check(k_cache, n_kv_heads, head_dim, n_seqs, context_lens, block_table,
                                     f"{y_heads} heads")
 
 
+def _kv8_err(err_count):
+    if err_count is None:
+        return
+    if err_count.dtype is not torch.int32:
+        raise QwError(QW_ERR_DTYPE, f"err_count must be int32, not {err_count.dtype}")
+    if err_count.numel() == 0:
+        raise QwError(QW_ERR_SHAPE, "err_count is empty")
+
+
 def _kv8_seqs(cu_seqlens_q) -> int:
     if cu_seqlens_q.dtype is not torch.int32:
         raise QwError(QW_ERR_DTYPE, f"cu_seqlens_q must be int32, not {cu_seqlens_q.dtype}")
@@ -338,6 +347,9 @@ def kv8_append(qkv, n_heads, n_kv_heads, head_dim, tp, positions, cos_sin, q_gam
         raise QwError(QW_ERR_DTYPE, "positions must be int64, cos_sin float32, gammas of qkv's type")
     if positions.numel() < qkv.shape[0] or cos_sin.numel() != cos_sin.shape[0] * head_dim:
         raise QwError(QW_ERR_SHAPE, f"{positions.numel()} positions and cos_sin {tuple(cos_sin.shape)} for {qkv.shape[0]} tokens")
+    if q_gamma.numel() < head_dim or k_gamma.numel() < head_dim:
+        raise QwError(QW_ERR_SHAPE, f"gammas of {q_gamma.numel()} and {k_gamma.numel()} weights for heads of {head_dim}")
+    _kv8_err(err_count)
     _check(load().qw_kv8_append(
         _dev_ptr(qkv, "qkv"), qkv.shape[0], n_heads, n_kv_heads, head_dim, tp, _dev_ptr(positions, "positions"),
         _dev_ptr(cos_sin, "cos_sin"), cos_sin.shape[0], _dev_ptr(q_gamma, "q_gamma"), _dev_ptr(k_gamma, "k_gamma"), eps,
@@ -355,6 +367,7 @@ def kv8_read(k_cache, v_cache, k_scale, v_scale, scale_block, rows, k_out, v_out
     n, out = rows.shape[0], k_out if k_out is not None else v_out
     if rows.dtype is not torch.int64 or (v_out is not None and v_out.dtype is not out.dtype):
         raise QwError(QW_ERR_DTYPE, "rows must be int64, k_out and v_out of one type")
+    _kv8_err(err_count)
     need = n * nkv * hd
     if (k_out is not None and k_out.numel() < need) or (v_out is not None and v_out.numel() < need):
         raise QwError(QW_ERR_SHAPE, f"outputs are smaller than {n} rows of {(nkv, hd)}")
