@@ -374,7 +374,7 @@ int qw_kv8_read(const void* k_cache, const void* v_cache, const float* k_scale, 
  *   workspace: *_workspace_size bytes, 16-byte aligned, zero-filled when
  *   allocated; may be NULL only when that size is 0.  Prefill leaves the first
  *   64 KiB alone, so that it can share one with decode, and needs at most 64 KiB
- *   + 152 x 256 x 130 floats for total_q <= n_seqs * max_seqlen_q.
+ *   + 152 x 256 x 130 floats, whatever the rows of padding in q.
  * qw_attention_decode_kv8: one query per sequence, at its last key.
  * qw_attention_prefill_kv8: causal attention of packed new tokens whose k and
  *   v are in the cache already (qw_kv8_append first).  total_q: rows of q;

@@ -397,7 +397,7 @@ def attention_decode_kv8(q, k_cache, v_cache, k_scale, v_scale, scale_block, con
         dtype_code(q.dtype), kv, _stream(stream)))
 
 
-# the largest workspace that attention_prefill_kv8 asks for (total_q <= n_seqs * max_seqlen_q)
+# the largest workspace that attention_prefill_kv8 asks for
 ATTENTION_PREFILL_KV8_WORKSPACE_MAX = 64 * 1024 + 152 * 256 * 130 * 4
 
 

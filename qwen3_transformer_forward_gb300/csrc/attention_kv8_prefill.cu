@@ -191,8 +191,9 @@ struct PrefillArgs {
   float scale_log2;     // |scale| log2 e
   float q_sign;         // sign of the scale
   bf16* out;
-  float* ws_o;          // [splits][total_q * nh][128]
-  float* ws_ml;         // [splits][total_q * nh][2]
+  int64_t part_rows;    // n_seqs * max_q * nh
+  float* ws_o;          // [splits][part_rows][128]
+  float* ws_ml;         // [splits][part_rows][2]
 };
 
 // Rows of one CTA (or one row of the merge): the sequence's packed rows from R0.
@@ -201,6 +202,11 @@ struct Rows {
   __device__ __forceinline__ int64_t id(const PrefillArgs& a, int R, int g) const {   // row of q and out
     const int tok = R / a.G;
     return (int64_t(qs) + tok) * a.nh + g * a.G + (R - tok * a.G);
+  }
+  // What takes a row of q and out of sequence s to its row in a part: parts have room for max_q
+  // tokens a sequence, so that rows of q that belong to none ask for none.
+  __device__ __forceinline__ int64_t to_part(const PrefillArgs& a, int s) const {
+    return (int64_t(s) * a.max_q - qs) * a.nh;
   }
 };
 __device__ __forceinline__ Rows rows_of(const PrefillArgs& a, int s) {
@@ -257,8 +263,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
   int s_u[2];   // steps of 64 keys: two a tile, without a last one that the unit does not see
 #pragma unroll
   for (int u = 0; u < 2; ++u) s_u[u] = 2 * n_u[u] - (n_u[u] > 0 && tile_key(n_u[u] - 1) + HALF >= hi_u[u] ? 1 : 0);
-  const int64_t n_rows_all = a.total_q * a.nh;
 
+  // row of this CTA's part for a row of q and out
+  auto part_row = [&](int64_t id) { return split * a.part_rows + id + rw.to_part(a, s); };
   // rows without a tile: zero output, or an empty part
   auto no_tiles = [&](int R, int n, int t, int step) {
     for (int i = t; i < n * 16; i += step) {
@@ -268,8 +275,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
       if (a.splits == 1) {
         *reinterpret_cast<uint4*>(a.out + id * HD + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
       } else if (c == 0) {
-        a.ws_ml[2 * (split * n_rows_all + id)] = -INFINITY;
-        a.ws_ml[2 * (split * n_rows_all + id) + 1] = 0.0f;
+        const int64_t at = part_row(id);
+        a.ws_ml[2 * at] = -INFINITY;
+        a.ws_ml[2 * at + 1] = 0.0f;
       }
     }
   };
@@ -676,7 +684,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prefill_kv8_kernel(const Pref
                 *reinterpret_cast<const uint4*>(sQ + tile_off(rr, cc));
         }
       } else {
-        const int64_t at = split * n_rows_all + id;
+        const int64_t at = part_row(id);
         const float fac = kUnshift;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -714,10 +722,10 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs a)
   const int lane = threadIdx.x & 31, R = int(blockIdx.x) * 8 + int(threadIdx.x >> 5), g = blockIdx.y;
   const Rows rw = rows_of(a, blockIdx.z);
   if (R >= rw.n) return;
-  const int64_t id = rw.id(a, R, g), n = a.total_q * a.nh;
+  const int64_t id = rw.id(a, R, g), part = id + rw.to_part(a, blockIdx.z), n = a.part_rows;
   const float2* ml = reinterpret_cast<const float2*>(a.ws_ml);
   float2 mine = make_float2(-INFINITY, 0.0f);   // part `lane` (at most 32)
-  if (lane < a.splits) mine = ml[lane * n + id];
+  if (lane < a.splits) mine = ml[lane * n + part];
   const float M = warp_max(mine.x);
   // A part without a visible key has (-inf, 0).  One of a query with NaN may have (-inf, NaN): its
   // weight is 0 too, but the NaN reaches l, and through l the row.
@@ -728,7 +736,7 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs a)
   for (int i = 0; i < a.splits; ++i) {
     const float wi = __shfl_sync(0xffffffffu, w, i);
     if (wi == 0.0f) continue;   // (an empty part has no O)
-    const float4 x = *(reinterpret_cast<const float4*>(a.ws_o + (i * n + id) * HD) + lane);
+    const float4 x = *(reinterpret_cast<const float4*>(a.ws_o + (i * n + part) * HD) + lane);
     acc.x = fmaf(x.x, wi, acc.x);
     acc.y = fmaf(x.y, wi, acc.y);
     acc.z = fmaf(x.z, wi, acc.z);
@@ -789,7 +797,7 @@ extern "C" size_t qw_attention_prefill_kv8_workspace_size(int n_seqs, int64_t to
                                                           int max_context, int n_heads, int n_kv_heads) {
   if (n_seqs <= 0 || total_q <= 0 || max_seqlen_q <= 0 || max_context < 0 || n_heads <= 0 || n_kv_heads <= 0) return 0;
   const int s = kv8p::prefill_splits(n_seqs, max_seqlen_q, max_context, n_heads, n_kv_heads);
-  return s == 1 ? 0 : kCounterBytes + size_t(s) * size_t(total_q) * n_heads * (kv8::HD + 2) * sizeof(float);
+  return s == 1 ? 0 : kCounterBytes + size_t(s) * n_seqs * max_seqlen_q * n_heads * (kv8::HD + 2) * sizeof(float);
 }
 
 extern "C" int qw_attention_prefill_kv8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -832,12 +840,13 @@ extern "C" int qw_attention_prefill_kv8(const void* q, const void* k_cache, cons
   a.G = n_heads / n_kv_heads;
   a.window = std::min(window, kv8::kMaxPositions);
   a.n_sink = std::min(n_sink, max_context);
+  a.part_rows = int64_t(n_seqs) * max_seqlen_q * n_heads;
   a.splits = kv8p::prefill_splits(n_seqs, max_seqlen_q, max_context, n_heads, n_kv_heads);
   a.scale_log2 = fabsf(scale) * kv8p::kLog2e;
   a.q_sign = scale < 0.0f ? -1.0f : 1.0f;
   a.out = static_cast<bf16*>(out);
   a.ws_o = need > 0 ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterBytes) : nullptr;   // (no counters here)
-  a.ws_ml = need > 0 ? a.ws_o + size_t(a.splits) * size_t(total_q) * n_heads * kv8::HD : nullptr;
+  a.ws_ml = need > 0 ? a.ws_o + a.splits * a.part_rows * kv8::HD : nullptr;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return kv_dtype == QW_I8 ? kv8p::launch<QW_I8>(a, n_seqs, st) : kv8p::launch<QW_E4M3>(a, n_seqs, st);
 }
