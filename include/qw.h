@@ -375,6 +375,10 @@ int qw_kv8_read(const void* k_cache, const void* v_cache, const float* k_scale, 
  *   allocated; may be NULL only when that size is 0.  Prefill leaves the first
  *   64 KiB alone, so that it can share one with decode, and needs at most 64 KiB
  *   + 152 x 256 x 130 floats, whatever the rows of padding in q.
+ * Only pages that some query of the call sees are read: a page wholly behind the
+ *   window of its sequence's first query, and past the n_sink first keys, may
+ *   have been dropped (a negative or any other entry in block_table) or belong
+ *   to another sequence by now.
  * qw_attention_decode_kv8: one query per sequence, at its last key.
  * qw_attention_prefill_kv8: causal attention of packed new tokens whose k and
  *   v are in the cache already (qw_kv8_append first).  total_q: rows of q;
