@@ -37,7 +37,10 @@ __device__ unsigned int g_kv8_error = 0;
 // scale: with x = score * log2 e * k_scale + log2(v_scale), the running maximum m
 // is over x, the weights are 2^(x - m + 15) <= 2^15 (f16 keeps 11 bits down to
 // 2^-29 of the largest), O takes the codes of V alone, and the denominator is
-// sum 2^(x - m) / v_scale, in fp32.
+// sum 2^(x - m) / v_scale, in fp32, of the weights before they are rounded.  One f16 is
+// enough: at most 2^-11 of a weight, independent for each key, against the 2^-8 that
+// the bf16 output is rounded by, and a second f16 for the rest would double the PV
+// products.  The exponentials and logarithms are the hardware's approximations (2^-22).
 // A (sequence, kv head) that ends inside one CTA is written out; otherwise every
 // CTA of it leaves (m, l, O) in the workspace slot (CTA + pair), distinct for each
 // that occurs, and the last to finish, by the pair's counter, adds them in CTA
@@ -134,7 +137,8 @@ __global__ void __launch_bounds__(DK_THREADS, 1) attn_decode_kv8_kernel(const __
                                                                        const __grid_constant__ CUtensorMap tmV,
                                                                        const DecodeArgs a) {
   constexpr int KS = DK_WARPS / HG, KT = 16 * KS, ST = dk_stages<HG, NT>();
-  constexpr int UN = NT == 1 ? 2 : 1;                // tiles of a consumer step (NT 2: no registers left for two)
+  // tiles of a consumer step (two n-tiles: one, and even so 84 to 108 bytes a thread are spilled; of one, none)
+  constexpr int UN = NT == 1 ? 2 : 1;
   constexpr uint32_t kBox = 16 * HG * HD;            // bytes of one TMA box
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));

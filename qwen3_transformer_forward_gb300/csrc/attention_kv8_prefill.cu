@@ -18,9 +18,12 @@
 //   warps 8-11    softmax of unit 0, warps 12-15 of unit 1: one row per thread
 // Block scales never touch the operands.  A block of 16 keys shares one scale,
 // so with x = score * log2 e * k_scale + log2(v_scale) the running maximum m is
-// over x, P = 2^(x - m + 7) is rounded to f16 (11 bits; m is raised lazily, when a
-// row's maximum grows by more than 2^8, so that P <= 2^15), O takes the codes of
-// V alone and the denominator is sum 2^(x - m) / v_scale in fp32.  q is moved by a
+// over x, P = 2^(x - m + 7) is rounded to f16 (m is raised lazily, when a row's
+// maximum grows by more than 2^8, so that P <= 2^15), O takes the codes of V alone
+// and the denominator is sum 2^(x - m) / v_scale in fp32, of the weights before they
+// are rounded.  P keeps 11 bits down to 2^-21 of the largest weight and 2^-32 of it
+// below: far under the 2^-8 of the bf16 output, and the A operand in TMEM holds f16.
+// The exponentials and logarithms are the hardware's approximations (2^-22).  q is moved by a
 // power of two per row (row_scale), exact in f16.  k_scale >= 0 and the softmax
 // scale's sign sits in q, so a block's largest x belongs to its largest score:
 // the maximum is taken over the raw scores.
@@ -33,8 +36,8 @@
 // pipe; the softmax's dependent steps (two warps on an SM sub-partition) and the
 // operand traffic through shared memory (Q is read again for each step, K and V are
 // written by the converters: about 2600 cycles of its bandwidth) hold it there.
-// 8 x 2048 tokens, 16 q / 8 kv heads, int8: 215 us, 640 TFLOP/s; 2 x 2500 new tokens
-// over 24000, 32 / 8 heads, e4m3, window 8192: 639 us, 960 TFLOP/s.
+// 8 x 2048 tokens, 16 q / 8 kv heads, int8: 213.5 us, 644 TFLOP/s; 2 x 2500 new tokens
+// over 24000, 32 / 8 heads, e4m3, window 8192: 643 us, 955 TFLOP/s.
 // Every mbarrier wait is bounded (2 s); on timeout the kernel records an error
 // word and runs to its end without waiting further, except for its own MMAs in flight.
 #include <math.h>
@@ -748,8 +751,10 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs a)
 }
 
 // Shares that the key tiles are cut into: as many as still fit the GPU's SMs at
-// once, with four tiles each at least.  (Rows that fill the SMs by themselves are
-// not split.)
+// once, with four tiles of max_context each at least.  The host knows neither the
+// lengths nor, here, the window: shares of a shorter or windowed sequence have fewer
+// tiles, down to none.  More CTAs than half the SMs are not split, and nor are rows that
+// fill the SMs by themselves.
 int prefill_splits(int n_seqs, int max_q, int max_ctx, int nh, int nkv) {
   constexpr int kSms = 152;
   const int64_t ctas = (int64_t(max_q) * (nh / nkv) + ROWS - 1) / ROWS * nkv * n_seqs;

@@ -35,7 +35,9 @@ __device__ __forceinline__ int seq_begin(const AppendArgs& a, int s) { return a.
 
 // The sequence and the scale block of block task `t`: sequences in order, each
 // with the blocks that its new tokens touch.  One warp scans the sequences 32
-// at a time.  s = -1 when there are fewer tasks.
+// at a time, a memory round trip each: nothing for tens of sequences, but every
+// task does it, so that its cost grows with the square of a large batch.  s = -1
+// when there are fewer tasks.
 __device__ __forceinline__ void find_block(const AppendArgs& a, int64_t t, int sb, int& s_out, int& blk_out) {
   const int lane = threadIdx.x & 31;
   int64_t before = 0;
@@ -256,10 +258,13 @@ template <int KV> __device__ __forceinline__ uint4 requant(const uint4& c, float
 // A block's tokens meet in one CTA because they share a scale: the block maxima of
 // k and of v are formed in shared memory and every value is quantised from the
 // registers that it was computed in, so each input is read once.  k and v
-// together, and two q heads on one RoPE row, keep enough loads in flight: 8 x 2048
+// together, and two q heads on one RoPE row, put more loads in flight: 8 x 2048
 // tokens of 16 q and 8 kv heads take 55.7 us, 4.2 TB/s (83 us with one of them at a
-// time; four q heads 65 us, one 61 us, 1024 threads an SM in each).  Bounded by the
-// issue of the norm, rotation and quantiser, about 20 instructions an element.
+// time; four q heads 65 us, one 61 us, 1024 threads an SM in each).  Neither issue
+// (65% of the slots, about 20 instructions an element) nor memory (DRAM at 51% of
+// the copy rate) is full: the largest stall is the wait for loads, which 1024 threads
+// of 64 registers cover in part.  The 64 are not enough for k, v and the gammas: 68 to
+// 76 bytes a thread are spilled and 92 read back, in every instantiation.
 constexpr int QH = 2;
 template <int KV, int SB>
 __global__ void __launch_bounds__(SB * 8, 1024 / (SB * 8)) kv8_append_kernel(const AppendArgs a) {
@@ -492,6 +497,8 @@ int launch_append(const AppendArgs& a0, cudaStream_t st) {
   // Up to eight tokens a sequence on average: warps instead of CTAs.  16 q and 8 kv
   // heads, scale_block 64: 64 sequences of one token 3.4 us against 7.4, of eight 5.8
   // against 11.3, 16 sequences of eight 4.2 against 4.1, of sixteen 6.4 against 5.0.
+  // (Only the average is known here: a long chunk among single tokens goes this way too,
+  // where its k and v are computed twice.)
   const bool few = a.T <= 8 * int64_t(a.n_seqs);
   a.kv_ctas = few ? (blocks * a.nkv * 2 + 3) / 4 : blocks * a.nkv;
   const int64_t q_ctas = few ? (a.T * a.nh + 15) / 16 : (a.T * ((a.nh + QH - 1) / QH) + SB - 1) / SB;
