@@ -375,8 +375,9 @@ int qw_kv8_read(const void* k_cache, const void* v_cache, const float* k_scale, 
  *   allocated; may be NULL only when that size is 0.  Prefill leaves the first
  *   64 KiB alone, so that it can share one with decode, and needs at most 64 KiB
  *   + 152 x 256 x 130 floats, whatever the rows of padding in q.
- * Weights are held relative to the query's largest weight * v_scale: a key 2^120
- *   below it (a v_scale of 0 counts as 2^-100) may be missing from the
+ * Weights are held relative to the query's largest weight * v_scale: in the sum of
+ *   the values to 2^-11 of themselves or 2^-32 of it, whichever is more, and a key
+ *   2^120 below it (a v_scale of 0 counts as 2^-100) may be missing from the
  *   denominator.
  * Only pages that some query of the call sees are read: a page wholly behind the
  *   window of its sequence's first query, and past the n_sink first keys, may
