@@ -6,7 +6,8 @@
  * RMSNorm, the linear layers (merged QKV and gate_up column splits, o_proj
  * and down_proj row splits), per-head QK-RMSNorm + RoPE + KV-cache store,
  * causal GQA attention for prefill and decode (over a bf16 or an 8-bit KV
- * cache), SiluAndMul and the vocab-sharded lm_head with greedy argmax.
+ * cache), SiluAndMul and the vocab-sharded lm_head with greedy argmax; the
+ * linear layers, the embedding and the lm_head also over 4-bit weights.
  *
  * Sources, cited by page and section:
  *   [VH]  devpress page "vocab 切 / head 切" (nano-vllm tensor parallelism):
@@ -590,6 +591,74 @@ int qw_sample(const void* logits, int64_t B, int64_t V, const float* temperature
               const float* uniforms, int64_t* out, void* workspace, size_t workspace_bytes, int dtype,
               void* stream);
 size_t qw_sample_workspace_size(int64_t B, int64_t V);
+
+/*
+ * Weights in 4 bits with group scales ([SK] §5, §6: the linear layers, the
+ * embedding and the lm_head at about a quarter of the bytes).  A matrix [N, K]
+ * is held as
+ *   codes   uint8 [N, K/2], 16-byte aligned: a code n in 0 .. 15 for each weight.
+ *           A row is K/8 little-endian 32-bit words; nibble p of word i (bits
+ *           4p .. 4p+3) is column 8i + 2p for p = 0 .. 3 and column
+ *           8i + 2(p - 4) + 1 for p = 4 .. 7
+ *   scales  bf16 [N, K/group]: s of each row and group of `group` consecutive
+ *           columns (32, 64 or 128)
+ *   zeros   uint8 [N, K/group]: zero points z, 0 .. 15; NULL: every z is 8
+ * and a weight is the bf16 number round((n - z) * s), rounded once: the weight
+ * that a bf16 checkpoint of the same matrix would hold.  Activations and outputs
+ * are bf16 (dtype QW_BF16).  K (for a row split K/tp) is a multiple of group.
+ * Errors: QW_ERR_DTYPE, QW_ERR_SHAPE (group, divisibility, sizes of 2^31 and
+ * more), QW_ERR_INVALID_ARG (null or misaligned pointers, negative sizes),
+ * QW_ERR_WORKSPACE.
+ *
+ * qw_w4_quantize: codes, scales and zeros of a matrix w bf16 [N, K], rounding
+ * to nearest even throughout.  For each row and group, over its finite weights:
+ *   zeros NULL: s = bf16(max|w| / 7);  n = clamp(round(w / s), -8, 7) + 8
+ *   zeros:      lo = min(w, 0), hi = max(w, 0), s = bf16((hi - lo) / 15),
+ *               z = min(round(-lo / s), 15), n = clamp(round(w / s) + z, 0, 15)
+ * where s is 0, w / 0 counts as w / 1.  NaN counts as 0, an infinity becomes the
+ * largest code of its sign.  A row split W [tp, N, K/tp] (qw_gemm) is quantised
+ * as tp * N rows of K/tp columns.
+ */
+int qw_w4_quantize(const void* w, int64_t N, int64_t K, int group, void* codes, void* scales, void* zeros, int dtype,
+                   void* stream);
+
+/*
+ * qw_embed_vocab from a 4-bit table [V, H]; with ids 0 .. V-1 the matrix's
+ * weights themselves.  ids, T, tp, out, err_count as there: an id outside
+ * [0, V) gives a zero row and counts in err_count.
+ */
+int qw_w4_embed_vocab(const int64_t* ids, int64_t T, const void* codes, const void* scales, const void* zeros, int64_t V,
+                      int64_t H, int group, int tp, void* out, int32_t* err_count, int dtype, void* stream);
+
+/*
+ * qw_gemm with 4-bit weights: C = A W^T, sums in fp32, rounded once.
+ *   QW_GEMM_COLUMN: codes of [N, K], any N that tp divides; with QW_EPI_SILU_MUL
+ *     the rows of shard r are [gate_r ; up_r], I/tp a multiple of 8, and
+ *     C [M, N/2] = silu(gate) * up is formed from the fp32 sums.
+ *   QW_GEMM_ROW_REDUCE: codes [tp, N, K/tp/2], scales and zeros
+ *     [tp, N, K/tp/group]; any N.
+ * Any M below 2^21.  A and C 16-byte aligned.  The weights may be read before
+ * the kernels enqueued earlier on the stream have ended, unless one of those
+ * is qw_w4_quantize or a kernel outside this library.
+ * workspace: qw_w4_gemm_workspace_size bytes; may be NULL when that is 0.
+ */
+int qw_w4_gemm(const void* A, const void* codes, const void* scales, const void* zeros, void* C, int64_t M, int64_t N,
+               int64_t K, int group, int tp, int mode, int epilogue, void* workspace, size_t workspace_bytes, int dtype,
+               void* stream);
+size_t qw_w4_gemm_workspace_size(int64_t M, int64_t N, int64_t K, int tp, int mode, int epilogue);
+
+/*
+ * qw_lm_head over a 4-bit table [V, H]: logits bf16 [n_out, V] of the rows
+ * last_idx[i] of hidden (NULL: rows 0 .. n_out-1; an index outside [0, T) is a
+ * zero row), and with next_tokens the argmax over each row of the rounded
+ * logits, lowest index on ties.  V any number that tp divides.
+ * workspace: qw_w4_lm_head_workspace_size bytes, 16-byte aligned; may be NULL
+ * when last_idx and next_tokens both are.
+ */
+int qw_w4_lm_head(const void* hidden, int64_t T, const int32_t* last_idx, int64_t n_out, const void* codes,
+                  const void* scales, const void* zeros, int64_t V, int64_t H, int group, int tp, void* logits,
+                  int64_t* next_tokens, void* workspace, size_t workspace_bytes, int dtype, void* stream);
+size_t qw_w4_lm_head_workspace_size(int64_t n_out, int64_t V, int64_t H, int tp);
 
 /*
  * One decode step of every decoder layer in one persistent kernel: for each

@@ -67,6 +67,12 @@ SIGNATURES = {
     "qw_argmax": (C.c_int, [_p, _i64, _i64, _p, _i32, _p]),
     "qw_sample": (C.c_int, [_p, _i64, _i64, _p, _p, _p, _p, _p, _sz, _i32, _p]),
     "qw_sample_workspace_size": (C.c_size_t, [_i64, _i64]),
+    "qw_w4_quantize": (C.c_int, [_p, _i64, _i64, _i32, _p, _p, _p, _i32, _p]),
+    "qw_w4_embed_vocab": (C.c_int, [_p, _i64, _p, _p, _p, _i64, _i64, _i32, _i32, _p, _p, _i32, _p]),
+    "qw_w4_gemm": (C.c_int, [_p, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _i32, _i32, _i32, _p, _sz, _i32, _p]),
+    "qw_w4_gemm_workspace_size": (C.c_size_t, [_i64, _i64, _i64, _i32, _i32, _i32]),
+    "qw_w4_lm_head": (C.c_int, [_p, _i64, _p, _i64, _p, _p, _p, _i64, _i64, _i32, _i32, _p, _p, _p, _sz, _i32, _p]),
+    "qw_w4_lm_head_workspace_size": (C.c_size_t, [_i64, _i64, _i64, _i32]),
     "qw_selftest_wait_timeout": (C.c_int, [_p]),
     "qw_add_rmsnorm_gemm": (C.c_int, [_p, _p, _p, _p, _f32, _p, _p, _i64, _i64, _i64, _i32, _i32, _i32, _p]),
     "qw_decode_layers": (C.c_int, [_p, _i32, _p, _p, _p, _p, _p, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _p,
@@ -470,6 +476,94 @@ def argmax(logits, out, stream=None):
     M, V = logits.shape
     _check(load().qw_argmax(_dev_ptr(logits, "logits"), M, V, _dev_ptr(out, "out"), dtype_code(logits.dtype),
                             _stream(stream)))
+
+
+def _w4_check(codes, scales, zeros, group, rows, columns):
+    """Types and sizes of a 4-bit matrix of `rows` stored rows of `columns`; the library sees pointers only."""
+    if codes.dtype is not torch.uint8 or scales.dtype is not torch.bfloat16:
+        raise QwError(QW_ERR_DTYPE, f"codes must be uint8 and scales bfloat16, not {codes.dtype} and {scales.dtype}")
+    per_row = columns // group if group > 0 else 0
+    groups = rows * per_row
+    if (codes.numel() * 2 != rows * columns or codes.shape[-1] * 2 != columns or scales.numel() != groups
+            or scales.shape[-1] != per_row):
+        raise QwError(QW_ERR_SHAPE, f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} are not {rows} rows of "
+                                    f"{columns} columns in groups of {group}")
+    if zeros is not None:
+        if zeros.dtype is not torch.uint8:
+            raise QwError(QW_ERR_DTYPE, f"zeros must be uint8, not {zeros.dtype}")
+        if zeros.numel() != groups or zeros.shape[-1] != per_row:
+            raise QwError(QW_ERR_SHAPE, f"zeros {tuple(zeros.shape)} are not {rows} rows of {per_row} groups")
+
+
+def _w4_bytes(workspace) -> int:
+    return workspace.numel() * workspace.element_size() if workspace is not None else 0
+
+
+def w4_quantize(w, group, codes, scales, zeros=None, stream=None):
+    """4-bit codes, bf16 group scales and (zeros given) zero points of w [N, K]."""
+    N, K = w.shape
+    _w4_check(codes, scales, zeros, group, N, K)
+    _check(load().qw_w4_quantize(_dev_ptr(w, "w"), N, K, group, _dev_ptr(codes, "codes"), _dev_ptr(scales, "scales"),
+                                 _dev_ptr(zeros, "zeros"), dtype_code(w.dtype), _stream(stream)))
+
+
+def w4_embed_vocab(ids, codes, scales, zeros, group, tp, out, err_count=None, stream=None):
+    """Rows of a 4-bit table [V, H] by id (int64 [T]) into out [T, H]."""
+    T, H = out.shape
+    V = codes.shape[0]
+    _w4_check(codes, scales, zeros, group, V, H)
+    if ids.dtype is not torch.int64:
+        raise QwError(QW_ERR_DTYPE, f"ids must be int64, not {ids.dtype}")
+    if ids.numel() != T:
+        raise QwError(QW_ERR_SHAPE, f"{ids.numel()} ids for {T} rows")
+    _kv8_err(err_count)
+    _check(load().qw_w4_embed_vocab(
+        _dev_ptr(ids, "ids"), T, _dev_ptr(codes, "codes"), _dev_ptr(scales, "scales"), _dev_ptr(zeros, "zeros"), V, H, group,
+        tp, _dev_ptr(out, "out"), _dev_ptr(err_count, "err_count"), dtype_code(out.dtype), _stream(stream)))
+
+
+def w4_gemm_workspace_size(M, N, K, tp, mode, epilogue) -> int:
+    return load().qw_w4_gemm_workspace_size(M, N, K, tp, mode, epilogue)
+
+
+def w4_gemm(A, codes, scales, zeros, C_out, N, group, tp=1, mode=QW_GEMM_COLUMN, epilogue=QW_EPI_NONE, workspace=None,
+            stream=None):
+    """gemm() with 4-bit weights; N: output features before SiluAndMul."""
+    M, K = A.shape
+    shards = tp if mode == QW_GEMM_ROW_REDUCE else 1
+    if tp > 0:
+        _w4_check(codes, scales, zeros, group, shards * N, K // shards)
+    if C_out.dtype is not A.dtype:
+        raise QwError(QW_ERR_DTYPE, f"the output's type {C_out.dtype} is not the input's, {A.dtype}")
+    if C_out.numel() != M * (N // 2 if epilogue == QW_EPI_SILU_MUL else N):
+        raise QwError(QW_ERR_SHAPE, f"output {tuple(C_out.shape)} for {M} tokens of {N} features")
+    _check(load().qw_w4_gemm(
+        _dev_ptr(A, "A"), _dev_ptr(codes, "codes"), _dev_ptr(scales, "scales"), _dev_ptr(zeros, "zeros"),
+        _dev_ptr(C_out, "C"), M, N, K, group, tp, mode, epilogue, _dev_ptr(workspace, "workspace"), _w4_bytes(workspace),
+        dtype_code(A.dtype), _stream(stream)))
+
+
+def w4_lm_head_workspace_size(n_out, V, H, tp) -> int:
+    return load().qw_w4_lm_head_workspace_size(n_out, V, H, tp)
+
+
+def w4_lm_head(hidden, last_idx, n_out, codes, scales, zeros, group, tp, logits, next_tokens=None, workspace=None,
+               stream=None):
+    """lm_head() over a 4-bit table [V, H]: logits of rows last_idx of hidden, and greedy tokens."""
+    T, H = hidden.shape
+    V = codes.shape[0]
+    _w4_check(codes, scales, zeros, group, V, H)
+    if logits.dtype is not hidden.dtype or (last_idx is not None and last_idx.dtype is not torch.int32) or (
+            next_tokens is not None and next_tokens.dtype is not torch.int64):
+        raise QwError(QW_ERR_DTYPE, "logits must be of hidden's type, last_idx int32, next_tokens int64")
+    if logits.numel() < n_out * V or (last_idx is not None and last_idx.numel() < n_out) or (
+            next_tokens is not None and next_tokens.numel() < n_out):
+        raise QwError(QW_ERR_SHAPE, f"logits, last_idx or next_tokens are smaller than {n_out} rows")
+    _check(load().qw_w4_lm_head(
+        _dev_ptr(hidden, "hidden"), T, _dev_ptr(last_idx, "last_idx"), n_out, _dev_ptr(codes, "codes"),
+        _dev_ptr(scales, "scales"), _dev_ptr(zeros, "zeros"), V, H, group, tp, _dev_ptr(logits, "logits"),
+        _dev_ptr(next_tokens, "next_tokens"), _dev_ptr(workspace, "workspace"), _w4_bytes(workspace),
+        dtype_code(hidden.dtype), _stream(stream)))
 
 
 def sample_workspace_size(B, V) -> int:

@@ -1,0 +1,271 @@
+// Linear layers with 4-bit weights, few tokens: weight streaming with warp-level MMA.
+#include "w4.cuh"
+
+namespace qw {
+
+template <typename T>
+int launch_gather_rows(const void* src, int64_t n_src, const int32_t* idx, int64_t n, int64_t H, void* out,
+                       cudaStream_t st);
+
+namespace w4 {
+
+int check_weights(const char* who, const void* codes, const void* scales, int64_t N, int64_t K, int group);
+Weights make_weights(const void* codes, const void* scales, const void* zeros, int64_t K, int group);
+
+struct GemvArgs {
+  const bf16* x;         // [M, K]
+  bf16* out;             // [M, ldc]
+  Weights w;             // of one shard's rows
+  int64_t rows;          // N: rows of a shard (row split), of the matrix (column)
+  int64_t ldc;
+  int64_t i_l;           // SiluAndMul: outputs of a shard
+  int64_t tiles;         // row tiles of 16 (SiluAndMul: 8 gate and their 8 up rows)
+  int M, K;
+  int pieces, pieces_l;  // pieces of K, of a shard's K
+  int split;             // warps that share a row tile, each every split-th chunk of 128 columns
+};
+
+__device__ __forceinline__ uint4 ldg_codes(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+constexpr int kWarps = 8;
+
+// A warp takes a tile of 16 weight rows and every split-th chunk of 128 columns; lane (g, t) = (lane / 4,
+// lane % 4) holds the 32 columns of piece t of rows g and g + 8.  The k index of an MMA may be any
+// permutation that weights and tokens share, so a lane's own columns are its k values: no shuffles.
+template <int NT, bool SILU>
+__global__ void __launch_bounds__(kWarps * 32) gemv_kernel(GemvArgs a) {
+  __shared__ float red[kWarps][16][NT * 8 + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int per_cta = kWarps / a.split, sl = warp % a.split;
+  const int64_t tile0 = int64_t(blockIdx.x) * per_cta, tile = tile0 + warp / a.split;
+  const int m0 = blockIdx.y * (NT * 8);
+  int64_t ra, rb;
+  bool oka = tile < a.tiles, okb = oka;
+  if (SILU) {
+    const int64_t o = tile * 8 + g, r = o / a.i_l;
+    ra = o + r * a.i_l;
+    rb = ra + a.i_l;
+  } else {
+    ra = tile * 16 + g;
+    rb = ra + 8;
+    oka = ra < a.rows;
+    okb = rb < a.rows;
+  }
+  float acc[NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
+  pdl_wait();
+  pdl_trigger();
+  int64_t shard = 0;           // first row of the shard's block
+  int ul = 4 * sl + t;         // piece within the shard
+  for (int u = ul; u - t < a.pieces; u += 4 * a.split, ul += 4 * a.split) {
+    while (ul >= a.pieces_l) {
+      ul -= a.pieces_l;
+      shard += a.rows;
+    }
+    const bool in = u < a.pieces;
+    uint4 ca = make_uint4(0, 0, 0, 0), cb = ca;
+    uint32_t sa = 0, sb = 0, za = 8, zb = 8;
+    const int grp = ul >> a.w.group_shift;
+    if (in && oka) {
+      ca = ldg_codes(a.w.codes + (shard + ra) * a.w.row_bytes + int64_t(ul) * 16);
+      sa = __ldg(reinterpret_cast<const uint16_t*>(a.w.scales) + (shard + ra) * a.w.groups + grp);
+      if (a.w.zeros != nullptr) za = __ldg(a.w.zeros + (shard + ra) * a.w.groups + grp);
+    }
+    if (in && okb) {
+      cb = ldg_codes(a.w.codes + (shard + rb) * a.w.row_bytes + int64_t(ul) * 16);
+      sb = __ldg(reinterpret_cast<const uint16_t*>(a.w.scales) + (shard + rb) * a.w.groups + grp);
+      if (a.w.zeros != nullptr) zb = __ldg(a.w.zeros + (shard + rb) * a.w.groups + grp);
+    }
+    const uint32_t sa2 = scale_pair(sa), sb2 = scale_pair(sb), za2 = offset_pair(za), zb2 = offset_pair(zb);
+    const uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t pa[4], pb[4];
+      decode(wa[i], za2, sa2, pa);
+      decode(wb[i], zb2, sb2, pb);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int tok = m0 + n * 8 + g;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (in && tok < a.M) x = __ldg(reinterpret_cast<const uint4*>(a.x + int64_t(tok) * a.K + u * kPiece + 8 * i));
+        mma_16816(acc[n], pa[0], pb[0], pa[1], pb[1], x.x, x.y);
+        mma_16816(acc[n], pa[2], pb[2], pa[3], pb[3], x.z, x.w);
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    red[warp][g][n * 8 + 2 * t] = acc[n][0];
+    red[warp][g][n * 8 + 2 * t + 1] = acc[n][1];
+    red[warp][g + 8][n * 8 + 2 * t] = acc[n][2];
+    red[warp][g + 8][n * 8 + 2 * t + 1] = acc[n][3];
+  }
+  __syncthreads();
+  const int out_rows = SILU ? 8 : 16;
+  for (int e = threadIdx.x; e < per_cta * out_rows * NT * 8; e += kWarps * 32) {
+    const int r = e % out_rows, lt = e / out_rows % per_cta, n = e / (out_rows * per_cta);
+    const int64_t o = (tile0 + lt) * out_rows + r;
+    if (m0 + n >= a.M || o >= (SILU ? a.rows / 2 : a.rows)) continue;
+    float v = 0.0f, up = 0.0f;
+    for (int s = 0; s < a.split; ++s) {   // in slice order
+      v += red[lt * a.split + s][r][n];
+      if (SILU) up += red[lt * a.split + s][r + 8][n];
+    }
+    if (SILU) v = __fdividef(v, 1.0f + __expf(-v)) * up;
+    a.out[int64_t(m0 + n) * a.ldc + o] = __float2bfloat16_rn(v);
+  }
+}
+
+template <int NT>
+static int launch_gemv(GemvArgs a, bool silu, cudaStream_t st) {
+  const int chunks = (a.pieces + 3) / 4;
+  a.split = 8;
+  while (a.split > 1 && (a.split > chunks || a.tiles * a.split > 152 * 32)) a.split >>= 1;
+  const int per_cta = kWarps / a.split;
+  const dim3 grid(unsigned((a.tiles + per_cta - 1) / per_cta), unsigned((a.M + NT * 8 - 1) / (NT * 8)));
+  if (grid.y > 65535) return set_error(QW_ERR_SHAPE, "qw_w4_gemm: too many tokens");
+  if (silu) launch_pdl(gemv_kernel<NT, true>, grid, kWarps * 32, 0, st, a);
+  else launch_pdl(gemv_kernel<NT, false>, grid, kWarps * 32, 0, st, a);
+  return check_launch("w4 gemv");
+}
+
+static int linear(const bf16* x, const void* codes, const void* scales, const void* zeros, bf16* out, int64_t M, int64_t N,
+                  int64_t K, int group, int tp, int mode, int epi, cudaStream_t st) {
+  const int64_t K_l = mode == QW_GEMM_ROW_REDUCE ? K / tp : K;
+  GemvArgs a{};
+  const bool silu = epi == QW_EPI_SILU_MUL;
+  a.x = x;
+  a.out = out;
+  a.w = make_weights(codes, scales, zeros, K_l, group);
+  a.rows = N;
+  a.ldc = silu ? N / 2 : N;
+  a.i_l = silu ? N / 2 / tp : 0;
+  a.tiles = silu ? N / 16 : (N + 15) / 16;
+  a.M = int(M);
+  a.K = int(K);
+  a.pieces = int(K / kPiece);
+  a.pieces_l = int(K_l / kPiece);
+  if (M <= 8) return launch_gemv<1>(a, silu, st);
+  if (M <= 16) return launch_gemv<2>(a, silu, st);
+  if (M <= 32) return launch_gemv<4>(a, silu, st);
+  return launch_gemv<8>(a, silu, st);
+}
+
+// argmax over rows of bf16 logits of any width, lowest index on ties (as qw_argmax; NaN is passed over)
+__global__ void __launch_bounds__(1024) argmax_kernel(const bf16* __restrict__ logits, int64_t V, int64_t* __restrict__ out) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float sv[32];
+  __shared__ int64_t si[32];
+  const bf16* p = logits + int64_t(blockIdx.x) * V;
+  float best = -INFINITY;
+  int64_t at = V;
+  auto take = [&](float ob, int64_t oi) {
+    if (ob > best || (ob == best && oi < at)) { best = ob; at = oi; }
+  };
+  for (int64_t i = threadIdx.x; i < V; i += 1024) {
+    const float f = __bfloat162float(p[i]);
+    if (f > best) { best = f; at = i; }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) take(__shfl_xor_sync(0xffffffffu, best, o), __shfl_xor_sync(0xffffffffu, at, o));
+  if ((threadIdx.x & 31) == 0) { sv[threadIdx.x >> 5] = best; si[threadIdx.x >> 5] = at; }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 32; ++w) take(sv[w], si[w]);
+    out[blockIdx.x] = at < V ? at : 0;
+  }
+}
+
+}  // namespace w4
+}  // namespace qw
+
+using namespace qw;
+
+static inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+extern "C" size_t qw_w4_gemm_workspace_size(int64_t M, int64_t N, int64_t K, int tp, int mode, int epilogue) {
+  (void)M, (void)N, (void)K, (void)tp, (void)mode, (void)epilogue;
+  return 0;
+}
+
+extern "C" int qw_w4_gemm(const void* A, const void* codes, const void* scales, const void* zeros, void* C, int64_t M,
+                          int64_t N, int64_t K, int group, int tp, int mode, int epilogue, void* workspace,
+                          size_t workspace_bytes, int dtype, void* stream) {
+  if (dtype != QW_BF16) return set_error(QW_ERR_DTYPE, "qw_w4_gemm: dtype %d", dtype);
+  if (M < 0 || N <= 0 || K <= 0 || tp <= 0) return set_error(QW_ERR_INVALID_ARG, "qw_w4_gemm: bad sizes");
+  if (mode != QW_GEMM_COLUMN && mode != QW_GEMM_ROW_REDUCE)
+    return set_error(QW_ERR_INVALID_ARG, "qw_w4_gemm: mode %d", mode);
+  if (epilogue != QW_EPI_NONE && epilogue != QW_EPI_SILU_MUL)
+    return set_error(QW_ERR_INVALID_ARG, "qw_w4_gemm: epilogue %d", epilogue);
+  if (epilogue == QW_EPI_SILU_MUL && mode != QW_GEMM_COLUMN)
+    return set_error(QW_ERR_INVALID_ARG, "qw_w4_gemm: SiluAndMul needs the column (gate_up) layout");
+  if (mode == QW_GEMM_ROW_REDUCE && K % tp) return set_error(QW_ERR_SHAPE, "qw_w4_gemm: K=%lld %% tp=%d", (long long)K, tp);
+  if (mode == QW_GEMM_COLUMN && N % tp) return set_error(QW_ERR_SHAPE, "qw_w4_gemm: N=%lld %% tp=%d", (long long)N, tp);
+  if (epilogue == QW_EPI_SILU_MUL && N % (16 * int64_t(tp)))
+    return set_error(QW_ERR_SHAPE, "qw_w4_gemm: gate_up width %lld not 2*tp*I_l with I_l a multiple of 8", (long long)N);
+  if (M >= (int64_t(1) << 21)) return set_error(QW_ERR_SHAPE, "qw_w4_gemm: 2^21 tokens or more");
+  if (M == 0) return QW_OK;
+  const int64_t K_l = mode == QW_GEMM_ROW_REDUCE ? K / tp : K;
+  if (K >= (int64_t(1) << 31)) return set_error(QW_ERR_SHAPE, "qw_w4_gemm: dimension too large");
+  const int rc = w4::check_weights("qw_w4_gemm", codes, scales, N, K_l, group);
+  if (rc) return rc;
+  if (!A || !C || !al16(A) || !al16(C)) return set_error(QW_ERR_INVALID_ARG, "qw_w4_gemm: null or misaligned A or C");
+  const size_t need = qw_w4_gemm_workspace_size(M, N, K, tp, mode, epilogue);
+  if (need && (!workspace || workspace_bytes < need))
+    return set_error(QW_ERR_WORKSPACE, "qw_w4_gemm: workspace of %zu bytes needed", need);
+  return w4::linear(static_cast<const bf16*>(A), codes, scales, zeros, static_cast<bf16*>(C), M, N, K, group, tp, mode,
+                    epilogue, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t qw_w4_lm_head_workspace_size(int64_t n_out, int64_t V, int64_t H, int tp) {
+  if (n_out <= 0 || V <= 0 || H <= 0) return 0;
+  (void)tp;
+  return kCounterBytes + (size_t(n_out) * size_t(H) * 2 + 255) / 256 * 256;
+}
+
+extern "C" int qw_w4_lm_head(const void* hidden, int64_t T, const int32_t* last_idx, int64_t n_out, const void* codes,
+                             const void* scales, const void* zeros, int64_t V, int64_t H, int group, int tp, void* logits,
+                             int64_t* next_tokens, void* workspace, size_t workspace_bytes, int dtype, void* stream) {
+  if (dtype != QW_BF16) return set_error(QW_ERR_DTYPE, "qw_w4_lm_head: dtype %d", dtype);
+  if (T < 0 || n_out < 0 || V <= 0 || H <= 0 || tp <= 0) return set_error(QW_ERR_INVALID_ARG, "qw_w4_lm_head: bad sizes");
+  if (V % tp) return set_error(QW_ERR_SHAPE, "qw_w4_lm_head: V=%lld %% tp=%d", (long long)V, tp);
+  if (n_out == 0) return QW_OK;
+  if (n_out >= (int64_t(1) << 21)) return set_error(QW_ERR_SHAPE, "qw_w4_lm_head: 2^21 rows or more");
+  if (!last_idx && n_out > T) return set_error(QW_ERR_SHAPE, "qw_w4_lm_head: n_out > T without last_idx");
+  const int rc = w4::check_weights("qw_w4_lm_head", codes, scales, V, H, group);
+  if (rc) return rc;
+  if (!hidden || !logits || !al16(hidden) || !al16(logits))
+    return set_error(QW_ERR_INVALID_ARG, "qw_w4_lm_head: null or misaligned hidden or logits");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const void* x = hidden;
+  const size_t need = qw_w4_lm_head_workspace_size(n_out, V, H, tp);
+  if ((last_idx || next_tokens) && (!workspace || workspace_bytes < need || !al16(workspace)))
+    return set_error(QW_ERR_WORKSPACE, "qw_w4_lm_head: workspace of %zu bytes needed", need);
+  if (last_idx) {
+    uint8_t* rows = static_cast<uint8_t*>(workspace) + kCounterBytes;
+    const int e = launch_gather_rows<bf16>(hidden, T, last_idx, n_out, H, rows, st);
+    if (e) return e;
+    x = rows;
+  }
+  int e = w4::linear(static_cast<const bf16*>(x), codes, scales, zeros, static_cast<bf16*>(logits), n_out, V, H, group, 1,
+                     QW_GEMM_COLUMN, QW_EPI_NONE, st);
+  if (e || !next_tokens) return e;
+  launch_pdl(w4::argmax_kernel, unsigned(n_out), 1024, 0, st, static_cast<const bf16*>(logits), V, next_tokens);
+  return check_launch("qw_w4_lm_head");
+}
