@@ -21,7 +21,7 @@ BUILD_DIR = ROOT / "_build"
 
 SOURCES = ["qw_api.cu", "elementwise.cu", "gemm.cu", "attention.cu", "attention_prefill.cu", "decode_step.cu",
            "sampler.cu", "kv8_cache.cu", "attention_kv8.cu",
-           "attention_kv8_prefill.cu", "w4_weights.cu", "w4_linear.cu"]
+           "attention_kv8_prefill.cu", "w4_weights.cu", "w4_linear.cu", "w4_gemm_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-warn-spills"]

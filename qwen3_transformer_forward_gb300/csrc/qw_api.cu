@@ -41,6 +41,7 @@ unsigned int take_attn_timeouts();
 unsigned int take_prefill_timeouts();
 unsigned int take_dstep_errors();
 unsigned int take_kv8_errors();
+unsigned int take_w4_errors();
 
 }  // namespace qw
 
@@ -53,13 +54,13 @@ extern "C" int qw_device_error(void* stream) {
   if (e != cudaSuccess) return qw::set_error(QW_ERR_CUDA, "qw_device_error: %s", cudaGetErrorString(e));
   const unsigned int gemm = qw::take_tc_timeouts(), dec_word = qw::take_attn_timeouts(),
                      pre = qw::take_prefill_timeouts(), step = qw::take_dstep_errors(),
-                     kv8_word = qw::take_kv8_errors();
+                     kv8_word = qw::take_kv8_errors(), w4 = qw::take_w4_errors();
   const unsigned int dec = dec_word & ~qw::kErrContextOverflow, kv8 = kv8_word & ~qw::kErrContextOverflow;
-  if (gemm | dec | pre | step | kv8)
+  if (gemm | dec | pre | step | kv8 | w4)
     return qw::set_error(QW_ERR_TIMEOUT,
                          "a bounded device-side wait timed out (gemm 0x%x, decode attention 0x%x, prefill attention "
-                         "0x%x, decode step 0x%x, 8-bit cache attention 0x%x)",
-                         gemm, dec, pre, step, kv8);
+                         "0x%x, decode step 0x%x, 8-bit cache attention 0x%x, 4-bit weights 0x%x)",
+                         gemm, dec, pre, step, kv8, w4);
   if ((dec_word | kv8_word) & qw::kErrContextOverflow)
     return qw::set_error(QW_ERR_INVALID_ARG,
                          "attention: a context_lens entry exceeded the call's max_context; the keys past it "

@@ -11,6 +11,8 @@ namespace w4 {
 
 int check_weights(const char* who, const void* codes, const void* scales, int64_t N, int64_t K, int group);
 Weights make_weights(const void* codes, const void* scales, const void* zeros, int64_t K, int group);
+int gemm_tc(const bf16* x, const Weights& w, bf16* out, int64_t M, int64_t N, int64_t K, int shards, int tp, bool silu,
+            cudaStream_t st);
 
 struct GemvArgs {
   const bf16* x;         // [M, K]
@@ -160,6 +162,7 @@ static int linear(const bf16* x, const void* codes, const void* scales, const vo
   a.K = int(K);
   a.pieces = int(K / kPiece);
   a.pieces_l = int(K_l / kPiece);
+  if (M > 64) return gemm_tc(x, a.w, out, M, N, K, mode == QW_GEMM_ROW_REDUCE ? tp : 1, tp, silu, st);
   if (M <= 8) return launch_gemv<1>(a, silu, st);
   if (M <= 16) return launch_gemv<2>(a, silu, st);
   if (M <= 32) return launch_gemv<4>(a, silu, st);
