@@ -2,8 +2,9 @@
 //
 // D[weight row, token] = W X^T: the weights are the MMA's A operand and lie in TMEM,
 // where the threads that decode them put them straight from registers; the tokens are B,
-// copied by TMA.  Shared memory then carries the tokens only, once in and once out for
-// each 128 weight rows.
+// copied by TMA.  Two CTAs (cta_group::2) share a tile of 256 weight rows: each decodes
+// 128 of them and holds half of the tokens, so that the tokens cross L2 and each shared
+// memory once for 256 rows.
 #include <algorithm>
 
 #include "tc_common.cuh"
@@ -14,11 +15,11 @@ namespace w4 {
 
 __device__ unsigned int g_w4_error = 0;
 
-constexpr int kRows = 128;          // weight rows of a tile (SiluAndMul: 64 gate rows and their up rows)
+constexpr int kRows = 128;          // weight rows of a CTA (SiluAndMul: 64 gate rows and their up rows), two CTAs a tile
 constexpr int kMaxTokens = 192;     // tokens of a tile: two accumulators and four stages of A fill TMEM
 constexpr int kThreads = 512;
-constexpr int XS = 6, CS = 3, AS = 4;                    // stages: tokens (64 columns), codes (256), decoded weights (64)
-constexpr uint32_t X_BYTES = kMaxTokens * 128, C_BYTES = kRows * 128;
+constexpr int XS = 8, CS = 4, AS = 4;                    // stages: tokens (64 columns), codes (256), decoded weights (64)
+constexpr uint32_t X_BYTES = kMaxTokens / 2 * 128, C_BYTES = kRows * 128;
 constexpr uint32_t OFF_X = 0, OFF_C = XS * X_BYTES, OFF_BAR = OFF_C + CS * C_BYTES;
 constexpr size_t kTcSmem = 1024 + OFF_BAR + 512;
 constexpr uint32_t kTmemCols = 512, kTmemA = 2 * kMaxTokens;
@@ -37,12 +38,43 @@ struct TcArgs {
   int shards, nk_l;       // shards of K, 64-column blocks of a shard
 };
 
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-               "r"(a), "l"(b_desc), "r"(idesc), "r"(acc)
-               : "memory");
+// The two CTAs of a pair: rank 0 issues the MMAs and holds the barriers that both feed.
+// Issued by the lane with `lead`, as a predicate: the warp stays converged and its operands in uniform registers (61 ->
+// 20 cycles an MMA, 110 -> 22 a commit, against one lane in a branch).
+__device__ __forceinline__ void umma_commit_pair(uint32_t lead, uint32_t bar) {   // arrives at this offset in both CTAs
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %0, 0;\n"
+      " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%1], %2;\n}\n" ::"r"(lead),
+      "r"(bar), "h"(uint16_t(3))
+      : "memory");
 }
-
+// B descriptors come as their low word and a constant high word
+__device__ __forceinline__ void umma_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                        uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 y;\n setp.ne.b32 q, %0, 0;\n setp.ne.b32 p, %6, 0;\n mov.b64 y, {%3, %4};\n"
+      " @q tcgen05.mma.cta_group::2.kind::f16 [%1], [%2], y, %5, p;\n}\n" ::"r"(lead),
+      "r"(d), "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r;
+}
+// A barrier of either CTA, by its cluster address.  What these arrivals hand over is TMEM, which the tcgen05 waits and
+// fences order: a release of all other memory to the cluster would cost about 800 cycles.
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// into this CTA's shared memory, completing on rank 0's barrier
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+      "[%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
 // 32 columns of TMEM, arrived (load and wait in one statement: no use can come between)
 __device__ __forceinline__ void tmem_ld32_arrived(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
@@ -66,12 +98,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile uint32_t* abort_flag = tmem_slot + 1;
   auto bar = [&](int b) { return bars + uint32_t(b) * 8u; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = int(cluster_rank()), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  auto lead_bar = [&](int b) { return map_to_rank(bar(b), 0); };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < XS; ++i) tcx::mbar_init(bar(B_X_FULL + i), 1), tcx::mbar_init(bar(B_X_EMPTY + i), 1);
     for (int i = 0; i < CS; ++i) tcx::mbar_init(bar(B_C_FULL + i), 1), tcx::mbar_init(bar(B_C_EMPTY + i), 8);
-    for (int i = 0; i < AS; ++i) tcx::mbar_init(bar(B_A_FULL + i), 4), tcx::mbar_init(bar(B_A_EMPTY + i), 1);
-    for (int i = 0; i < 2; ++i) tcx::mbar_init(bar(B_ACC_FULL + i), 1), tcx::mbar_init(bar(B_ACC_EMPTY + i), 4);
+    for (int i = 0; i < AS; ++i) tcx::mbar_init(bar(B_A_FULL + i), 8), tcx::mbar_init(bar(B_A_EMPTY + i), 1);
+    for (int i = 0; i < 2; ++i) tcx::mbar_init(bar(B_ACC_FULL + i), 1), tcx::mbar_init(bar(B_ACC_EMPTY + i), 8);
     tcx::mbar_init(bar(B_DRAIN), 1);
     *abort_flag = 0;
     tcx::fence_mbar_init();
@@ -79,11 +113,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tcx::prefetch_map(&tm_c);
   }
   if (warp == 1) {
-    tcx::tmem_alloc(smem_u32(tmem_slot), kTmemCols);
-    tcx::tmem_relinquish();
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   tcx::tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  cluster_sync_all();   // both CTAs' barriers and TMEM are there
   tcx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -104,9 +140,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tiles = a.p_tiles * a.q_tiles, ncs_l = (a.nk_l + 3) / 4;
   // first weight row (gate row) of a row tile; the stored rows of shard r of K begin at r * rows
   auto tile_row = [&](int p) -> int64_t {
-    if (!SILU) return int64_t(p) * kRows;
+    if (!SILU) return (int64_t(p) * 2 + rank) * kRows;
     const int r = p / a.shard_tiles;
-    return int64_t(r) * 2 * a.i_l + int64_t(p % a.shard_tiles) * (kRows / 2);
+    return int64_t(r) * 2 * a.i_l + (int64_t(p % a.shard_tiles) * 2 + rank) * (kRows / 2);
   };
 
   if (warp == 0) {
@@ -125,9 +161,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++cs;
       };
       bool waited = false;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+      for (int tile = pair; tile < tiles && ok; tile += pairs) {
         const int64_t row = tile_row(tile % a.p_tiles);
-        const int m0 = tile / a.p_tiles * a.bn;
+        const int m0 = tile / a.p_tiles * a.bn + rank * (a.bn / 2);
         for (int r = 0; r < a.shards && ok; ++r)
           for (int c = 0; c < ncs_l && ok; ++c) {
             load_codes(row, r, c);
@@ -139,42 +175,45 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t s = xs % XS;
               ok = wait(B_X_EMPTY + s, ((xs / XS) & 1) ^ 1, 2u);
               if (!ok) break;
-              tcx::mbar_expect_tx(bar(B_X_FULL + s), uint32_t(a.bn) * 128u);
-              tcx::tma_load_3d(sx + s * X_BYTES, &tm_x, bar(B_X_FULL + s), kb * 64, r, m0);
+              if (rank == 0) tcx::mbar_expect_tx(bar(B_X_FULL + s), uint32_t(a.bn) * 128u);   // both halves
+              tma_load_3d_pair(sx + s * X_BYTES, &tm_x, lead_bar(B_X_FULL + s), kb * 64, r, m0);
               ++xs;
             }
           }
       }
       if (!ok) {   // the copies in flight land before the block ends
         for (uint32_t i = cs > CS ? cs - CS : 0; i < cs; ++i) tcx::mbar_wait(bar(B_C_FULL + i % CS), (i / CS) & 1, &g_w4_error, 1u);
-        for (uint32_t i = xs > XS ? xs - XS : 0; i < xs; ++i) tcx::mbar_wait(bar(B_X_FULL + i % XS), (i / XS) & 1, &g_w4_error, 2u);
+        for (uint32_t i = xs > XS ? xs - XS : 0; i < xs && rank == 0; ++i) tcx::mbar_wait(bar(B_X_FULL + i % XS), (i / XS) & 1, &g_w4_error, 2u);
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---- MMA ----
-      const uint32_t idesc = tcx::idesc_bf16(kRows, a.bn);
+    if (rank == 0) {
+      // ---- MMA, for both CTAs ----
+      const uint32_t lead = elect_one();
+      const uint32_t idesc = tcx::idesc_bf16(2 * kRows, a.bn);
+      const uint64_t desc = tcx::sw128_desc(sx);
+      const uint32_t b_lo = uint32_t(desc), b_hi = uint32_t(desc >> 32);
       const int nk = a.shards * a.nk_l;
       uint32_t it = 0, u = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, ++u) {
+      for (int tile = pair; tile < tiles && ok; tile += pairs, ++u) {
         const uint32_t d = tmem + (u & 1) * kMaxTokens;
-        ok = wait(B_ACC_EMPTY + (u & 1), ((u >> 1) & 1) ^ 1, 4u);
+        ok = __all_sync(0xffffffffu, wait(B_ACC_EMPTY + (u & 1), ((u >> 1) & 1) ^ 1, 4u));
         for (int kb = 0; kb < nk && ok; ++kb, ++it) {
           const uint32_t s = it % XS, as = it % AS;
-          ok = wait(B_X_FULL + s, (it / XS) & 1, 8u) && wait(B_A_FULL + as, (it / AS) & 1, 16u);
+          ok = __all_sync(0xffffffffu, wait(B_X_FULL + s, (it / XS) & 1, 8u) && wait(B_A_FULL + as, (it / AS) & 1, 16u));
           if (!ok) break;
           tcx::tc_fence_after();
-          const uint64_t b = tcx::sw128_desc(sx + s * X_BYTES);
+          const uint32_t b = b_lo + s * (X_BYTES >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            umma_ts(d, tmem + kTmemA + as * 32 + k * 8, b + uint64_t(2 * k), idesc, (kb > 0 || k > 0) ? 1u : 0u);
-          tcx::umma_commit(bar(B_X_EMPTY + s));
-          tcx::umma_commit(bar(B_A_EMPTY + as));
+            umma_ts(lead, d, tmem + kTmemA + as * 32 + k * 8, b + 2 * k, b_hi, idesc, (kb > 0 || k > 0) ? 1u : 0u);
+          umma_commit_pair(lead, bar(B_X_EMPTY + s));
+          umma_commit_pair(lead, bar(B_A_EMPTY + as));
         }
-        if (ok) tcx::umma_commit(bar(B_ACC_FULL + (u & 1)));
+        if (ok) umma_commit_pair(lead, bar(B_ACC_FULL + (u & 1)));
       }
-      tcx::umma_commit(bar(B_DRAIN));
+      umma_commit_pair(lead, bar(B_DRAIN));
       tcx::mbar_wait(bar(B_DRAIN), 0, &g_w4_error, 32u);
     }
   } else if (warp >= 4 && warp < 12) {
@@ -185,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint16_t* scales = reinterpret_cast<const uint16_t*>(a.w.scales);
     uint32_t cs = 0, it0 = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+    for (int tile = pair; tile < tiles && ok; tile += pairs) {
       const int p = tile % a.p_tiles;
       int64_t row = tile_row(p);
       row += SILU ? (lane >> 4) * a.i_l + 16 * q + (lane & 15) : srow;
@@ -246,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tcx::tmem_st_wait();
             tcx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) tcx::mbar_arrive(bar(B_A_FULL + as));
+            if (lane == 0) arrive_cluster(lead_bar(B_A_FULL + as));
           }
         }
       }
@@ -257,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3;
     uint32_t u = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, ++u) {
+    for (int tile = pair; tile < tiles && ok; tile += pairs, ++u) {
       ok = __all_sync(0xffffffffu, wait(B_ACC_FULL + (u & 1), (u >> 1) & 1, 256u));
       if (!ok) break;
       tcx::tc_fence_after();
@@ -266,11 +305,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       int64_t o;       // output column of this thread
       bool have;
       if (SILU) {
-        const int64_t j = int64_t(p % a.shard_tiles) * (kRows / 2) + 16 * q + (lane & 15);
+        const int64_t j = (int64_t(p % a.shard_tiles) * 2 + rank) * (kRows / 2) + 16 * q + (lane & 15);
         o = int64_t(p / a.shard_tiles) * a.i_l + j;
         have = j < a.i_l;
       } else {
-        o = int64_t(p) * kRows + 32 * q + lane;
+        o = (int64_t(p) * 2 + rank) * kRows + 32 * q + lane;
         have = o < a.rows;
       }
       for (int c = 0; c < a.bn; c += 32) {
@@ -295,15 +334,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tcx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) tcx::mbar_arrive(bar(B_ACC_EMPTY + (u & 1)));
+      if (lane == 0) arrive_cluster(lead_bar(B_ACC_EMPTY + (u & 1)));
     }
   }
   __syncwarp();
   tcx::tc_fence_before();
-  __syncthreads();
+  cluster_sync_all();   // neither CTA leaves while the other may arrive at its barriers or use its TMEM
   if (warp == 1) {
     tcx::tc_fence_after();
-    tcx::tmem_dealloc(tmem, kTmemCols);
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
 }
 
@@ -314,7 +353,22 @@ static int launch(const CUtensorMap& mx, const CUtensorMap& mc, const TcArgs& a,
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kTcSmem));
   if (set != cudaSuccess) return set_error(QW_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(set));
   const int tiles = a.p_tiles * a.q_tiles;
-  launch_pdl(kern, unsigned(std::min(tiles, 152)), kThreads, kTcSmem, st, mx, mc, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(2 * std::min(tiles, 76)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kTcSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mx, mc, a);
+  if (e != cudaSuccess) return set_error(QW_ERR_CUDA, "w4 gemm_tc_kernel launch: %s", cudaGetErrorString(e));
   return check_launch("w4 gemm_tc_kernel");
 }
 
@@ -331,15 +385,15 @@ int gemm_tc(const bf16* x, const Weights& w, bf16* out, int64_t M, int64_t N, in
   a.q_tiles = int((M + kMaxTokens - 1) / kMaxTokens);
   a.bn = int((M + a.q_tiles - 1) / a.q_tiles + 15) / 16 * 16;
   a.q_tiles = int((M + a.bn - 1) / a.bn);
-  a.shard_tiles = silu ? int((a.i_l + kRows / 2 - 1) / (kRows / 2)) : 0;
-  const int64_t p_tiles = silu ? int64_t(tp) * a.shard_tiles : (N + kRows - 1) / kRows;
+  a.shard_tiles = silu ? int((a.i_l + kRows - 1) / kRows) : 0;
+  const int64_t p_tiles = silu ? int64_t(tp) * a.shard_tiles : (N + 2 * kRows - 1) / (2 * kRows);
   if (p_tiles * a.q_tiles >= (int64_t(1) << 31)) return set_error(QW_ERR_SHAPE, "qw_w4_gemm: too many output tiles");
   a.p_tiles = int(p_tiles);
   a.shards = shards;
   a.nk_l = int((K_l + 63) / 64);
   CUtensorMap mx, mc;
   const uint64_t xd[3] = {uint64_t(K_l), uint64_t(shards), uint64_t(M)}, xst[2] = {uint64_t(K_l) * 2, uint64_t(K) * 2};
-  const uint32_t xb[3] = {64, 1, uint32_t(a.bn)};
+  const uint32_t xb[3] = {64, 1, uint32_t(a.bn / 2)};
   int rc = make_tensor_map(&mx, x, 3, xd, xst, xb);
   if (rc) return rc;
   // codes as 2-byte elements: 64 of them are 256 columns
