@@ -17,7 +17,8 @@ __device__ unsigned int g_w4_error = 0;
 
 constexpr int kRows = 128;          // weight rows of a CTA (SiluAndMul: 64 gate rows and their up rows), two CTAs a tile
 constexpr int kMaxTokens = 192;     // tokens of a tile: two accumulators and four stages of A fill TMEM
-constexpr int kThreads = 512;
+constexpr int kSets = 3;            // sets of four decoding warps, which take the 64-column blocks in turn
+constexpr int kDecode0 = 4, kEpilogue0 = kDecode0 + 4 * kSets, kThreads = 32 * (kEpilogue0 + 4);
 constexpr int XS = 8, CS = 4, AS = 4;                    // stages: tokens (64 columns), codes (256), decoded weights (64)
 constexpr uint32_t X_BYTES = kMaxTokens / 2 * 128, C_BYTES = kRows * 128;
 constexpr uint32_t OFF_X = 0, OFF_C = XS * X_BYTES, OFF_BAR = OFF_C + CS * C_BYTES;
@@ -67,14 +68,29 @@ __device__ __forceinline__ uint32_t elect_one() {
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// into this CTA's shared memory, completing on rank 0's barrier
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+// copies into this CTA's shared memory: completing on its own barrier, and on rank 0's
+__device__ __forceinline__ void tma_load(uint32_t lead, uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
-      "[%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      "{\n .reg .pred q;\n setp.ne.b32 q, %0, 0;\n"
+      " @q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%1], [%2, {%4, %5, %6}], [%3];\n}\n" ::"r"(lead),
+      "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
+__device__ __forceinline__ void tma_load_pair(uint32_t lead, uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y,
+                                              int z) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %0, 0;\n"
+      " @q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%1], [%2, {%4, %5, %6}], "
+      "[%3];\n}\n" ::"r"(lead),
+      "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void expect_tx(uint32_t lead, uint32_t bar, uint32_t bytes) {
+  asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %0, 0;\n @q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%1], %2;\n}\n" ::"r"(lead),
+               "r"(bar), "r"(bytes)
+               : "memory");
+}
+
 // 32 columns of TMEM, arrived (load and wait in one statement: no use can come between)
 __device__ __forceinline__ void tmem_ld32_arrived(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
@@ -88,7 +104,7 @@ __device__ __forceinline__ void tmem_ld32_arrived(uint32_t taddr, uint32_t (&r)[
       : "memory");
 }
 
-template <bool SILU>
+template <bool SILU, int GS>   // GS: log2 of a group's pieces of 32 columns
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_c, TcArgs a) {
   extern __shared__ uint8_t smem_dyn[];
@@ -103,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < XS; ++i) tcx::mbar_init(bar(B_X_FULL + i), 1), tcx::mbar_init(bar(B_X_EMPTY + i), 1);
-    for (int i = 0; i < CS; ++i) tcx::mbar_init(bar(B_C_FULL + i), 1), tcx::mbar_init(bar(B_C_EMPTY + i), 8);
+    for (int i = 0; i < CS; ++i) tcx::mbar_init(bar(B_C_FULL + i), 1), tcx::mbar_init(bar(B_C_EMPTY + i), 16);
     for (int i = 0; i < AS; ++i) tcx::mbar_init(bar(B_A_FULL + i), 8), tcx::mbar_init(bar(B_A_EMPTY + i), 1);
     for (int i = 0; i < 2; ++i) tcx::mbar_init(bar(B_ACC_FULL + i), 1), tcx::mbar_init(bar(B_ACC_EMPTY + i), 8);
     tcx::mbar_init(bar(B_DRAIN), 1);
@@ -146,46 +162,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ---- TMA: code stages ahead of the token stages that they go with ----
-      uint32_t cs = 0, xs = 0;
-      bool ok = true;
-      auto load_codes = [&](int64_t row, int r, int c) {
-        const uint32_t s = cs % CS;
-        ok = wait(B_C_EMPTY + s, ((cs / CS) & 1) ^ 1, 1u);
-        if (!ok) return;
-        tcx::mbar_expect_tx(bar(B_C_FULL + s), C_BYTES);
-        const uint32_t dst = sc + s * C_BYTES;
-        tcx::tma_load_3d(dst, &tm_c, bar(B_C_FULL + s), c * 64, int(row), r);
-        if (SILU) tcx::tma_load_3d(dst + C_BYTES / 2, &tm_c, bar(B_C_FULL + s), c * 64, int(row + a.i_l), r);
-        ++cs;
-      };
-      bool waited = false;
-      for (int tile = pair; tile < tiles && ok; tile += pairs) {
-        const int64_t row = tile_row(tile % a.p_tiles);
-        const int m0 = tile / a.p_tiles * a.bn + rank * (a.bn / 2);
-        for (int r = 0; r < a.shards && ok; ++r)
-          for (int c = 0; c < ncs_l && ok; ++c) {
-            load_codes(row, r, c);
-            if (!waited) {
-              pdl_wait();   // the tokens may come from the kernel before; the weights are constants
-              waited = true;
-            }
-            for (int kb = 4 * c; kb < min(4 * c + 4, a.nk_l) && ok; ++kb) {
-              const uint32_t s = xs % XS;
-              ok = wait(B_X_EMPTY + s, ((xs / XS) & 1) ^ 1, 2u);
-              if (!ok) break;
-              if (rank == 0) tcx::mbar_expect_tx(bar(B_X_FULL + s), uint32_t(a.bn) * 128u);   // both halves
-              tma_load_3d_pair(sx + s * X_BYTES, &tm_x, lead_bar(B_X_FULL + s), kb * 64, r, m0);
-              ++xs;
-            }
-          }
-      }
-      if (!ok) {   // the copies in flight land before the block ends
-        for (uint32_t i = cs > CS ? cs - CS : 0; i < cs; ++i) tcx::mbar_wait(bar(B_C_FULL + i % CS), (i / CS) & 1, &g_w4_error, 1u);
-        for (uint32_t i = xs > XS ? xs - XS : 0; i < xs && rank == 0; ++i) tcx::mbar_wait(bar(B_X_FULL + i % XS), (i / XS) & 1, &g_w4_error, 2u);
-      }
+    // ---- tokens: this CTA's half of each block ----
+    const uint32_t lead = elect_one();
+    uint32_t n = 0;
+    bool ok = true;
+    pdl_wait();   // the tokens may come from the kernel before; the weights are constants
+    for (int tile = pair; tile < tiles && ok; tile += pairs) {
+      const int m0 = tile / a.p_tiles * a.bn + rank * (a.bn / 2);
+      for (int r = 0; r < a.shards && ok; ++r)
+        for (int kb = 0; kb < a.nk_l; ++kb, ++n) {
+          const uint32_t s = n % XS;
+          ok = __all_sync(0xffffffffu, wait(B_X_EMPTY + s, ((n / XS) & 1) ^ 1, 2u));
+          if (!ok) break;
+          if (rank == 0) expect_tx(lead, bar(B_X_FULL + s), uint32_t(a.bn) * 128u);   // both halves
+          tma_load_pair(lead, sx + s * X_BYTES, &tm_x, lead_bar(B_X_FULL + s), kb * 64, r, m0);
+        }
     }
+    if (!ok && rank == 0)   // the copies in flight land before the block ends
+      for (uint32_t i = n > XS ? n - XS : 0; i < n; ++i) tcx::mbar_wait(bar(B_X_FULL + i % XS), (i / XS) & 1, &g_w4_error, 2u);
+  } else if (warp == 2) {
+    // ---- codes: 256 columns of this CTA's rows at a time ----
+    const uint32_t lead = elect_one();
+    uint32_t n = 0;
+    bool ok = true;
+    for (int tile = pair; tile < tiles && ok; tile += pairs) {
+      const int row = int(tile_row(tile % a.p_tiles));
+      for (int r = 0; r < a.shards && ok; ++r)
+        for (int c = 0; c < ncs_l; ++c, ++n) {
+          const uint32_t s = n % CS, dst = sc + s * C_BYTES;
+          ok = __all_sync(0xffffffffu, wait(B_C_EMPTY + s, ((n / CS) & 1) ^ 1, 1u));
+          if (!ok) break;
+          expect_tx(lead, bar(B_C_FULL + s), C_BYTES);
+          tma_load(lead, dst, &tm_c, bar(B_C_FULL + s), c * 64, row, r);
+          if (SILU) tma_load(lead, dst + C_BYTES / 2, &tm_c, bar(B_C_FULL + s), c * 64, row + int(a.i_l), r);
+        }
+    }
+    if (!ok)
+      for (uint32_t i = n > CS ? n - CS : 0; i < n; ++i) tcx::mbar_wait(bar(B_C_FULL + i % CS), (i / CS) & 1, &g_w4_error, 1u);
   } else if (warp == 1) {
     if (rank == 0) {
       // ---- MMA, for both CTAs ----
@@ -216,89 +229,100 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma_commit_pair(lead, bar(B_DRAIN));
       tcx::mbar_wait(bar(B_DRAIN), 0, &g_w4_error, 32u);
     }
-  } else if (warp >= 4 && warp < 12) {
-    // ---- decode: one weight row a thread; four warps cover the rows, two such sets take the 64-column blocks in turn ----
-    const int q = warp & 3, h = (warp - 4) >> 2;
+  } else if (warp >= kDecode0 && warp < kEpilogue0) {
+    // ---- decode: one weight row a thread, four warps the rows of a block of 64 columns ----
+    const int q = warp & 3, set = (warp - kDecode0) >> 2;
     const int srow = SILU ? (lane >> 4) * 64 + 16 * q + (lane & 15) : 32 * q + lane;   // row in the code stage
-    const uint32_t lane_base = uint32_t(32 * q) << 16;
+    const int64_t row_off = SILU ? (lane >> 4) * a.i_l + 16 * q + (lane & 15) : srow;
+    const uint32_t code_row = sc + uint32_t(srow) * 128u, tmem_row = tmem + (uint32_t(32 * q) << 16) + kTmemA;
     const uint16_t* scales = reinterpret_cast<const uint16_t*>(a.w.scales);
-    uint32_t cs = 0, it0 = 0;
-    bool ok = true;
-    for (int tile = pair; tile < tiles && ok; tile += pairs) {
-      const int p = tile % a.p_tiles;
-      int64_t row = tile_row(p);
-      row += SILU ? (lane >> 4) * a.i_l + 16 * q + (lane & 15) : srow;
-      const bool have = row < a.rows;
-      for (int r = 0; r < a.shards && ok; ++r) {
-        const int64_t g0 = (int64_t(r) * a.rows + row) * a.w.groups;
-        for (int c = 0; c < ncs_l && ok; ++c, ++cs) {
-          const int kend = min(4 * c + 4, a.nk_l);
-          // scales of this warp's two blocks: two pieces of 32 columns in each
-          uint32_t s[2][2], z[2][2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int g = ((4 * c + 2 * j + h) * 2 + e) >> a.w.group_shift;
-              const bool in = have && g < a.w.groups;
-              s[j][e] = in ? __ldg(scales + g0 + g) : 0u;
-              z[j][e] = in && a.w.zeros != nullptr ? __ldg(a.w.zeros + g0 + g) : 8u;
-            }
-          const uint32_t st = cs % CS;
-          ok = __all_sync(0xffffffffu, wait(B_C_FULL + st, (cs / CS) & 1, 64u));   // the warp goes on as one
-          if (!ok) break;
-          uint4 v[2][2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t ch = uint32_t((2 * j + h) * 2 + e);
-              const uint32_t addr = sc + st * C_BYTES + uint32_t(srow) * 128u + ((ch ^ uint32_t(srow & 7)) << 4);
-              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                           : "=r"(v[j][e].x), "=r"(v[j][e].y), "=r"(v[j][e].z), "=r"(v[j][e].w)
-                           : "r"(addr));
-            }
-          __syncwarp();
-          if (lane == 0) tcx::mbar_arrive(bar(B_C_EMPTY + st));
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int kb = 4 * c + 2 * j + h;
-            if (kb >= kend) break;
-            uint32_t w[32];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t s2 = scale_pair(s[j][e]), z2 = offset_pair(z[j][e]);
-              const uint32_t word[4] = {v[j][e].x, v[j][e].y, v[j][e].z, v[j][e].w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t o[4];
-                decode(word[i], z2, s2, o);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) w[16 * e + 4 * i + k] = o[k];
-              }
-            }
-            const uint32_t it = it0 + uint32_t(r * a.nk_l + kb), as = it % AS;
-            ok = __all_sync(0xffffffffu, wait(B_A_EMPTY + as, ((it / AS) & 1) ^ 1, 128u));
-            if (!ok) break;
-            tcx::tc_fence_after();
-            tcx::tmem_st32(tmem + lane_base + kTmemA + as * 32, w);
-            tcx::tmem_st_wait();
-            tcx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_cluster(lead_bar(B_A_FULL + as));
-          }
+    // the block: its tile, shard r of K, place kb in the shard; cs0: code stages before this shard of this tile
+    int tile = pair, r = 0, kb = set;
+    uint32_t it = set, cs0 = 0;
+    const uint16_t* sp = nullptr;   // scales (and offset of the zeros) of this thread's row in the block's shard
+    int64_t zo = 0;
+    bool have = false;
+    auto settle = [&]() {   // kb may lie past its shard
+      while (kb >= a.nk_l) {
+        kb -= a.nk_l;
+        cs0 += ncs_l;
+        if (++r == a.shards) {
+          r = 0;
+          tile += pairs;
         }
       }
-      it0 += uint32_t(a.shards * a.nk_l);
+      if (tile >= tiles) return;
+      const int64_t row = tile_row(tile % a.p_tiles) + row_off;
+      have = row < a.rows;
+      zo = (int64_t(r) * a.rows + row) * a.w.groups;
+      sp = scales + zo;
+    };
+    // scale and zero point of the block's two pieces of 32 columns, the scale 0 where there is none
+    uint32_t s[2], z[2];
+    auto load_scales = [&]() {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (GS > 0 && e == 1) {   // one group
+          s[1] = s[0];
+          z[1] = z[0];
+          break;
+        }
+        const int g = (2 * kb + e) >> GS;
+        const bool in = have && g < a.w.groups;
+        s[e] = in ? __ldg(sp + g) : 0u;
+        z[e] = in && a.w.zeros != nullptr ? __ldg(a.w.zeros + zo + g) : 8u;
+      }
+    };
+    settle();
+    if (tile < tiles) load_scales();
+    while (tile < tiles) {
+      const uint32_t cs = cs0 + uint32_t(kb >> 2), st = cs % CS, as = it % AS, in_stage = uint32_t(kb & 3);
+      const bool last = kb == a.nk_l - 1;
+      const uint32_t s2[2] = {scale_pair(s[0]), scale_pair(s[1])}, z2[2] = {offset_pair(z[0]), offset_pair(z[1])};
+      const uint32_t a_parity = ((it / AS) & 1) ^ 1;
+      it += kSets;
+      kb += kSets;
+      if (kb >= a.nk_l) settle();
+      if (tile < tiles) load_scales();   // of this warp's next block, in flight meanwhile
+      if (!__all_sync(0xffffffffu, wait(B_C_FULL + st, (cs / CS) & 1, 64u))) break;   // the warp goes on as one
+      uint4 v[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v[e].x), "=r"(v[e].y), "=r"(v[e].z), "=r"(v[e].w)
+                     : "r"(code_row + st * C_BYTES + (((2 * in_stage + e) ^ uint32_t(srow & 7)) << 4)));
+      uint32_t w[32];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t word[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t o[4];
+          decode(word[i], z2[e], s2[e], o);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[16 * e + 4 * i + k] = o[k];
+        }
+      }
+      __syncwarp();
+      // a stage is free after 16 arrivals: of the four warps of each of its blocks, the last block's for those it lacks
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar(B_C_EMPTY + st)), "r"(last ? 4u - in_stage : 1u)
+                     : "memory");
+      if (!__all_sync(0xffffffffu, wait(B_A_EMPTY + as, a_parity, 128u))) break;
+      tcx::tc_fence_after();
+      tcx::tmem_st32(tmem_row + as * 32, w);
+      tcx::tmem_st_wait();
+      tcx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(lead_bar(B_A_FULL + as));
     }
-  } else if (warp >= 12) {
+  } else if (warp >= kEpilogue0) {
     // ---- epilogue ----
     const int q = warp & 3;
+    const bool even = (a.ldc & 1) == 0;   // two outputs of a token make an aligned word
     uint32_t u = 0;
-    bool ok = true;
-    for (int tile = pair; tile < tiles && ok; tile += pairs, ++u) {
-      ok = __all_sync(0xffffffffu, wait(B_ACC_FULL + (u & 1), (u >> 1) & 1, 256u));
-      if (!ok) break;
+    for (int tile = pair; tile < tiles; tile += pairs, ++u) {
+      if (!__all_sync(0xffffffffu, wait(B_ACC_FULL + (u & 1), (u >> 1) & 1, 256u))) break;
       tcx::tc_fence_after();
       const int p = tile % a.p_tiles, m0 = tile / a.p_tiles * a.bn, m1 = min(m0 + a.bn, a.M);
       const uint32_t d = tmem + (uint32_t(32 * q) << 16) + (u & 1) * kMaxTokens;
@@ -312,29 +336,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         o = (int64_t(p) * 2 + rank) * kRows + 32 * q + lane;
         have = o < a.rows;
       }
+      const bool pairs_of = !SILU && even && (int64_t(p) * 2 + rank) * kRows + 32 * q + 32 <= a.rows;
       for (int c = 0; c < a.bn; c += 32) {
         uint32_t v[32];
         tmem_ld32_arrived(d + c, v);
+        if (c + 32 >= a.bn) {   // the accumulator is read out
+          tcx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_cluster(lead_bar(B_ACC_EMPTY + (u & 1)));
+        }
+        const int left = m1 - m0 - c;   // tokens of these columns
         if (SILU) {
           // lanes 0-15 hold the gate, 16-31 the up of output (lane & 15); the halves take tokens in turn
+          bf16* to = a.out + int64_t(m0 + c + (lane >> 4)) * a.ldc + o;
+          bf16 y[16];
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float give = __uint_as_float(lane < 16 ? v[i + 1] : v[i]);
+          for (int i = 0; i < 16; ++i) {   // all before the stores, whose conditions would keep them apart
+            const float give = __uint_as_float(lane < 16 ? v[2 * i + 1] : v[2 * i]);
             const float got = __shfl_xor_sync(0xffffffffu, give, 16);
-            const float gate = lane < 16 ? __uint_as_float(v[i]) : got;
-            const float up = lane < 16 ? got : __uint_as_float(v[i + 1]);
-            const int m = m0 + c + i + (lane >> 4);
-            if (have && m < m1) a.out[int64_t(m) * a.ldc + o] = __float2bfloat16_rn(__fdividef(gate, 1.0f + __expf(-gate)) * up);
+            const float gate = lane < 16 ? __uint_as_float(v[2 * i]) : got;
+            const float up = lane < 16 ? got : __uint_as_float(v[2 * i + 1]);
+            y[i] = __float2bfloat16_rn(__fdividef(gate, 1.0f + __expf(-gate)) * up);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i, to += 2 * a.ldc)
+            if (have && 2 * i + (lane >> 4) < left) *to = y[i];
+        } else if (pairs_of) {
+          // lanes in twos exchange halves: the even one stores both columns of token i, the odd one of token i + 1
+          const uint32_t sel = lane & 1 ? 0x3276u : 0x5410u;
+          bf16* to = a.out + int64_t(m0 + c + (lane & 1)) * a.ldc + (o & ~int64_t(1));
+#pragma unroll
+          for (int i = 0; i < 32; i += 2, to += 2 * a.ldc) {
+            const uint32_t mine = pack_bf16(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+            if (i + (lane & 1) < left) *reinterpret_cast<uint32_t*>(to) = __byte_perm(mine, other, sel);
           }
         } else {
+          bf16* to = a.out + int64_t(m0 + c) * a.ldc + o;
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (have && m0 + c + i < m1) a.out[int64_t(m0 + c + i) * a.ldc + o] = __float2bfloat16_rn(__uint_as_float(v[i]));
+          for (int i = 0; i < 32; ++i, to += a.ldc)
+            if (have && i < left) *to = __float2bfloat16_rn(__uint_as_float(v[i]));
         }
       }
-      tcx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_cluster(lead_bar(B_ACC_EMPTY + (u & 1)));
     }
   }
   __syncwarp();
@@ -346,9 +389,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool SILU>
+template <bool SILU, int GS>
 static int launch(const CUtensorMap& mx, const CUtensorMap& mc, const TcArgs& a, cudaStream_t st) {
-  auto kern = gemm_tc_kernel<SILU>;
+  auto kern = gemm_tc_kernel<SILU, GS>;
   static const cudaError_t set =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kTcSmem));
   if (set != cudaSuccess) return set_error(QW_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(set));
@@ -402,7 +445,11 @@ int gemm_tc(const bf16* x, const Weights& w, bf16* out, int64_t M, int64_t N, in
   const uint32_t cb[3] = {64, silu ? 64u : 128u, 1};
   rc = make_tensor_map(&mc, w.codes, 3, cd, cst, cb);
   if (rc) return rc;
-  return silu ? launch<true>(mx, mc, a, st) : launch<false>(mx, mc, a, st);
+  switch (w.group_shift) {
+    case 0: return silu ? launch<true, 0>(mx, mc, a, st) : launch<false, 0>(mx, mc, a, st);
+    case 1: return silu ? launch<true, 1>(mx, mc, a, st) : launch<false, 1>(mx, mc, a, st);
+    default: return silu ? launch<true, 2>(mx, mc, a, st) : launch<false, 2>(mx, mc, a, st);
+  }
 }
 
 }  // namespace w4
