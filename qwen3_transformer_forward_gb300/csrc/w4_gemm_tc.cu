@@ -17,15 +17,15 @@ __device__ unsigned int g_w4_error = 0;
 
 constexpr int kRows = 128;          // weight rows of a CTA (SiluAndMul: 64 gate rows and their up rows), two CTAs a tile
 constexpr int kMaxTokens = 192;     // tokens of a tile: two accumulators and four stages of A fill TMEM
-constexpr int kSets = 3;            // sets of four decoding warps, which take the 64-column blocks in turn
+constexpr int kSets = 4;            // sets of four decoding warps, which take the 64-column blocks in turn
 constexpr int kDecode0 = 4, kEpilogue0 = kDecode0 + 4 * kSets, kThreads = 32 * (kEpilogue0 + 4);
-constexpr int XS = 8, CS = 4, AS = 4;                    // stages: tokens (64 columns), codes (256), decoded weights (64)
-constexpr uint32_t X_BYTES = kMaxTokens / 2 * 128, C_BYTES = kRows * 128;
+constexpr int XS = 4, CS = 4, AS = 4;   // stages: tokens (128 columns), codes (256), decoded weights (64, two a step)
+constexpr uint32_t X_HALF = kMaxTokens / 2 * 128, X_BYTES = 2 * X_HALF, C_BYTES = kRows * 128;
 constexpr uint32_t OFF_X = 0, OFF_C = XS * X_BYTES, OFF_BAR = OFF_C + CS * C_BYTES;
 constexpr size_t kTcSmem = 1024 + OFF_BAR + 512;
 constexpr uint32_t kTmemCols = 512, kTmemA = 2 * kMaxTokens;
 constexpr int B_X_FULL = 0, B_X_EMPTY = B_X_FULL + XS, B_C_FULL = B_X_EMPTY + XS, B_C_EMPTY = B_C_FULL + CS,
-              B_A_FULL = B_C_EMPTY + CS, B_A_EMPTY = B_A_FULL + AS, B_ACC_FULL = B_A_EMPTY + AS, B_ACC_EMPTY = B_ACC_FULL + 2,
+              B_A_FULL = B_C_EMPTY + CS, B_A_EMPTY = B_A_FULL + AS / 2, B_ACC_FULL = B_A_EMPTY + AS, B_ACC_EMPTY = B_ACC_FULL + 2,
               B_DRAIN = B_ACC_EMPTY + 2, N_BARS = B_DRAIN + 1;
 static_assert(N_BARS * 8 + 8 <= 512, "barrier area");
 
@@ -58,6 +58,15 @@ __device__ __forceinline__ void umma_ts(uint32_t lead, uint32_t d, uint32_t a, u
       "r"(d), "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
       : "memory");
 }
+__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {   // without the wait
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t r;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
@@ -65,8 +74,8 @@ __device__ __forceinline__ uint32_t elect_one() {
 }
 // A barrier of either CTA, by its cluster address.  What these arrivals hand over is TMEM, which the tcgen05 waits and
 // fences order: a release of all other memory to the cluster would cost about 800 cycles.
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void arrive_cluster(uint32_t bar, uint32_t count = 1) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
 // copies into this CTA's shared memory: completing on its own barrier, and on rank 0's
 __device__ __forceinline__ void tma_load(uint32_t lead, uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
@@ -120,7 +129,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < XS; ++i) tcx::mbar_init(bar(B_X_FULL + i), 1), tcx::mbar_init(bar(B_X_EMPTY + i), 1);
     for (int i = 0; i < CS; ++i) tcx::mbar_init(bar(B_C_FULL + i), 1), tcx::mbar_init(bar(B_C_EMPTY + i), 16);
-    for (int i = 0; i < AS; ++i) tcx::mbar_init(bar(B_A_FULL + i), 8), tcx::mbar_init(bar(B_A_EMPTY + i), 1);
+    for (int i = 0; i < AS; ++i) tcx::mbar_init(bar(B_A_EMPTY + i), 1);
+    for (int i = 0; i < AS / 2; ++i) tcx::mbar_init(bar(B_A_FULL + i), 16);
     for (int i = 0; i < 2; ++i) tcx::mbar_init(bar(B_ACC_FULL + i), 1), tcx::mbar_init(bar(B_ACC_EMPTY + i), 8);
     tcx::mbar_init(bar(B_DRAIN), 1);
     *abort_flag = 0;
@@ -170,12 +180,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int tile = pair; tile < tiles && ok; tile += pairs) {
       const int m0 = tile / a.p_tiles * a.bn + rank * (a.bn / 2);
       for (int r = 0; r < a.shards && ok; ++r)
-        for (int kb = 0; kb < a.nk_l; ++kb, ++n) {
-          const uint32_t s = n % XS;
-          ok = __all_sync(0xffffffffu, wait(B_X_EMPTY + s, ((n / XS) & 1) ^ 1, 2u));
+        for (int kb = 0; kb < a.nk_l; kb += 2, ++n) {
+          const uint32_t s = n % XS, dst = sx + s * X_BYTES;
+          const bool two = kb + 1 < a.nk_l;
+          ok = wait(B_X_EMPTY + s, ((n / XS) & 1) ^ 1, 2u);
           if (!ok) break;
-          if (rank == 0) expect_tx(lead, bar(B_X_FULL + s), uint32_t(a.bn) * 128u);   // both halves
-          tma_load_pair(lead, sx + s * X_BYTES, &tm_x, lead_bar(B_X_FULL + s), kb * 64, r, m0);
+          if (rank == 0) expect_tx(lead, bar(B_X_FULL + s), uint32_t(a.bn) * (two ? 256u : 128u));   // both CTAs' halves
+          tma_load_pair(lead, dst, &tm_x, lead_bar(B_X_FULL + s), kb * 64, r, m0);
+          if (two) tma_load_pair(lead, dst + X_HALF, &tm_x, lead_bar(B_X_FULL + s), kb * 64 + 64, r, m0);
         }
     }
     if (!ok && rank == 0)   // the copies in flight land before the block ends
@@ -190,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int r = 0; r < a.shards && ok; ++r)
         for (int c = 0; c < ncs_l; ++c, ++n) {
           const uint32_t s = n % CS, dst = sc + s * C_BYTES;
-          ok = __all_sync(0xffffffffu, wait(B_C_EMPTY + s, ((n / CS) & 1) ^ 1, 1u));
+          ok = wait(B_C_EMPTY + s, ((n / CS) & 1) ^ 1, 1u);
           if (!ok) break;
           expect_tx(lead, bar(B_C_FULL + s), C_BYTES);
           tma_load(lead, dst, &tm_c, bar(B_C_FULL + s), c * 64, row, r);
@@ -206,24 +218,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc = tcx::idesc_bf16(2 * kRows, a.bn);
       const uint64_t desc = tcx::sw128_desc(sx);
       const uint32_t b_lo = uint32_t(desc), b_hi = uint32_t(desc >> 32);
-      const int nk = a.shards * a.nk_l;
-      uint32_t it = 0, u = 0;
-      bool ok = true;
+      uint32_t n = 0, u = 0;           // n: steps of two blocks
+      bool ok = true, ready = false;   // ready: this step's operands were seen there while the one before was issued
       for (int tile = pair; tile < tiles && ok; tile += pairs, ++u) {
         const uint32_t d = tmem + (u & 1) * kMaxTokens;
-        ok = __all_sync(0xffffffffu, wait(B_ACC_EMPTY + (u & 1), ((u >> 1) & 1) ^ 1, 4u));
-        for (int kb = 0; kb < nk && ok; ++kb, ++it) {
-          const uint32_t s = it % XS, as = it % AS;
-          ok = __all_sync(0xffffffffu, wait(B_X_FULL + s, (it / XS) & 1, 8u) && wait(B_A_FULL + as, (it / AS) & 1, 16u));
-          if (!ok) break;
-          tcx::tc_fence_after();
-          const uint32_t b = b_lo + s * (X_BYTES >> 4);
+        uint32_t add = 0;
+        ok = wait(B_ACC_EMPTY + (u & 1), ((u >> 1) & 1) ^ 1, 4u);
+        for (int r = 0; r < a.shards && ok; ++r)
+          for (int kb = 0; kb < a.nk_l; kb += 2, ++n) {
+            const uint32_t s = n % XS, h = n & 1;
+            if (!ready) ok = wait(B_X_FULL + s, (n / XS) & 1, 8u) && wait(B_A_FULL + h, (n >> 1) & 1, 16u);
+            if (!ok) break;
+            tcx::tc_fence_after();
+            const uint32_t n1 = n + 1;
+            const bool x1 = test_wait(bar(B_X_FULL + n1 % XS), (n1 / XS) & 1), a1 = test_wait(bar(B_A_FULL + (n1 & 1)), (n1 >> 1) & 1);
+            const uint32_t b = b_lo + s * (X_BYTES >> 4), at = tmem + kTmemA + h * 64;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_ts(lead, d, tmem + kTmemA + as * 32 + k * 8, b + 2 * k, b_hi, idesc, (kb > 0 || k > 0) ? 1u : 0u);
-          umma_commit_pair(lead, bar(B_X_EMPTY + s));
-          umma_commit_pair(lead, bar(B_A_EMPTY + as));
-        }
+            for (int k = 0; k < 4; ++k) {
+              umma_ts(lead, d, at + k * 8, b + 2 * k, b_hi, idesc, add);
+              add = 1;
+            }
+            umma_commit_pair(lead, bar(B_A_EMPTY + 2 * h));
+            if (kb + 1 < a.nk_l)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) umma_ts(lead, d, at + 32 + k * 8, b + (X_HALF >> 4) + 2 * k, b_hi, idesc, 1u);
+            umma_commit_pair(lead, bar(B_A_EMPTY + 2 * h + 1));
+            umma_commit_pair(lead, bar(B_X_EMPTY + s));
+            ready = x1 && a1;
+          }
         if (ok) umma_commit_pair(lead, bar(B_ACC_FULL + (u & 1)));
       }
       umma_commit_pair(lead, bar(B_DRAIN));
@@ -236,9 +258,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t row_off = SILU ? (lane >> 4) * a.i_l + 16 * q + (lane & 15) : srow;
     const uint32_t code_row = sc + uint32_t(srow) * 128u, tmem_row = tmem + (uint32_t(32 * q) << 16) + kTmemA;
     const uint16_t* scales = reinterpret_cast<const uint16_t*>(a.w.scales);
-    // the block: its tile, shard r of K, place kb in the shard; cs0: code stages before this shard of this tile
+    // the block: its tile, shard r of K, place kb in the shard; cs0, n0: code stages and MMA steps before this shard
     int tile = pair, r = 0, kb = set;
-    uint32_t it = set, cs0 = 0;
+    uint32_t cs0 = 0, n0 = 0;
     const uint16_t* sp = nullptr;   // scales (and offset of the zeros) of this thread's row in the block's shard
     int64_t zo = 0;
     bool have = false;
@@ -246,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (kb >= a.nk_l) {
         kb -= a.nk_l;
         cs0 += ncs_l;
+        n0 += (a.nk_l + 1) / 2;
         if (++r == a.shards) {
           r = 0;
           tile += pairs;
@@ -276,11 +299,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     settle();
     if (tile < tiles) load_scales();
     while (tile < tiles) {
-      const uint32_t cs = cs0 + uint32_t(kb >> 2), st = cs % CS, as = it % AS, in_stage = uint32_t(kb & 3);
+      const uint32_t cs = cs0 + uint32_t(kb >> 2), st = cs % CS, in_stage = uint32_t(kb & 3);
+      const uint32_t n = n0 + uint32_t(kb >> 1), slot = 2 * (n & 1) + uint32_t(kb & 1), a_parity = ((n >> 1) & 1) ^ 1;
       const bool last = kb == a.nk_l - 1;
       const uint32_t s2[2] = {scale_pair(s[0]), scale_pair(s[1])}, z2[2] = {offset_pair(z[0]), offset_pair(z[1])};
-      const uint32_t a_parity = ((it / AS) & 1) ^ 1;
-      it += kSets;
+      const uint32_t arrivals = last && !(kb & 1) ? 2 : 1;   // for the block that its step lacks, too
       kb += kSets;
       if (kb >= a.nk_l) settle();
       if (tile < tiles) load_scales();   // of this warp's next block, in flight meanwhile
@@ -308,13 +331,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0)
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar(B_C_EMPTY + st)), "r"(last ? 4u - in_stage : 1u)
                      : "memory");
-      if (!__all_sync(0xffffffffu, wait(B_A_EMPTY + as, a_parity, 128u))) break;
+      if (!__all_sync(0xffffffffu, wait(B_A_EMPTY + slot, a_parity, 128u))) break;
       tcx::tc_fence_after();
-      tcx::tmem_st32(tmem_row + as * 32, w);
+      tcx::tmem_st32(tmem_row + slot * 32, w);
       tcx::tmem_st_wait();
       tcx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_cluster(lead_bar(B_A_FULL + as));
+      if (lane == 0) arrive_cluster(lead_bar(B_A_FULL + (n & 1)), arrivals);
     }
   } else if (warp >= kEpilogue0) {
     // ---- epilogue ----
