@@ -17,9 +17,12 @@ __device__ unsigned int g_w4_error = 0;
 
 constexpr int kRows = 128;          // weight rows of a CTA (SiluAndMul: 64 gate rows and their up rows), two CTAs a tile
 constexpr int kMaxTokens = 192;     // tokens of a tile: two accumulators and four stages of A fill TMEM
-constexpr int kSets = 4;            // sets of four decoding warps, which take the 64-column blocks in turn
-constexpr int kDecode0 = 4, kEpilogue0 = kDecode0 + 4 * kSets, kThreads = 32 * (kEpilogue0 + 4);
 constexpr int XS = 4, CS = 4, AS = 4;   // stages: tokens (128 columns), codes (256), decoded weights (64, two a step)
+constexpr int kSets = 4;            // sets of four decoding warps, which take the 64-column blocks in turn
+// A set's next block lies kSets on and waits for the MMAs of the block AS before that one.  With kSets <= AS it is
+// among those that the set's last block waited for, or that block itself, so a parity is never two phases old.
+static_assert(kSets <= AS && AS == 4, "");
+constexpr int kDecode0 = 4, kEpilogue0 = kDecode0 + 4 * kSets, kThreads = 32 * (kEpilogue0 + 4);
 constexpr uint32_t X_HALF = kMaxTokens / 2 * 128, X_BYTES = 2 * X_HALF, C_BYTES = kRows * 128;
 constexpr uint32_t OFF_X = 0, OFF_C = XS * X_BYTES, OFF_BAR = OFF_C + CS * C_BYTES;
 constexpr size_t kTcSmem = 1024 + OFF_BAR + 512;
@@ -36,7 +39,7 @@ struct TcArgs {
   int M, bn;              // tokens, tokens of a tile
   int p_tiles, q_tiles;   // weight row tiles, token tiles
   int shard_tiles;        // SiluAndMul: row tiles of a shard
-  int shards, nk_l;       // shards of K, 64-column blocks of a shard
+  int shards, nk_l;       // shards of K, 64-column blocks of a shard (even: a last one may hold zeros)
 };
 
 // The two CTAs of a pair: rank 0 issues the MMAs and holds the barriers that both feed.
@@ -74,8 +77,8 @@ __device__ __forceinline__ uint32_t elect_one() {
 }
 // A barrier of either CTA, by its cluster address.  What these arrivals hand over is TMEM, which the tcgen05 waits and
 // fences order: a release of all other memory to the cluster would cost about 800 cycles.
-__device__ __forceinline__ void arrive_cluster(uint32_t bar, uint32_t count = 1) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // copies into this CTA's shared memory: completing on its own barrier, and on rank 0's
 __device__ __forceinline__ void tma_load(uint32_t lead, uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
@@ -182,12 +185,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int r = 0; r < a.shards && ok; ++r)
         for (int kb = 0; kb < a.nk_l; kb += 2, ++n) {
           const uint32_t s = n % XS, dst = sx + s * X_BYTES;
-          const bool two = kb + 1 < a.nk_l;
           ok = wait(B_X_EMPTY + s, ((n / XS) & 1) ^ 1, 2u);
           if (!ok) break;
-          if (rank == 0) expect_tx(lead, bar(B_X_FULL + s), uint32_t(a.bn) * (two ? 256u : 128u));   // both CTAs' halves
+          if (rank == 0) expect_tx(lead, bar(B_X_FULL + s), uint32_t(a.bn) * 256u);   // both CTAs' halves
           tma_load_pair(lead, dst, &tm_x, lead_bar(B_X_FULL + s), kb * 64, r, m0);
-          if (two) tma_load_pair(lead, dst + X_HALF, &tm_x, lead_bar(B_X_FULL + s), kb * 64 + 64, r, m0);
+          tma_load_pair(lead, dst + X_HALF, &tm_x, lead_bar(B_X_FULL + s), kb * 64 + 64, r, m0);
         }
     }
     if (!ok && rank == 0)   // the copies in flight land before the block ends
@@ -239,9 +241,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               add = 1;
             }
             umma_commit_pair(lead, bar(B_A_EMPTY + 2 * h));
-            if (kb + 1 < a.nk_l)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) umma_ts(lead, d, at + 32 + k * 8, b + (X_HALF >> 4) + 2 * k, b_hi, idesc, 1u);
+            for (int k = 0; k < 4; ++k) umma_ts(lead, d, at + 32 + k * 8, b + (X_HALF >> 4) + 2 * k, b_hi, idesc, 1u);
             umma_commit_pair(lead, bar(B_A_EMPTY + 2 * h + 1));
             umma_commit_pair(lead, bar(B_X_EMPTY + s));
             ready = x1 && a1;
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (kb >= a.nk_l) {
         kb -= a.nk_l;
         cs0 += ncs_l;
-        n0 += (a.nk_l + 1) / 2;
+        n0 += a.nk_l / 2;
         if (++r == a.shards) {
           r = 0;
           tile += pairs;
@@ -303,7 +304,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t n = n0 + uint32_t(kb >> 1), slot = 2 * (n & 1) + uint32_t(kb & 1), a_parity = ((n >> 1) & 1) ^ 1;
       const bool last = kb == a.nk_l - 1;
       const uint32_t s2[2] = {scale_pair(s[0]), scale_pair(s[1])}, z2[2] = {offset_pair(z[0]), offset_pair(z[1])};
-      const uint32_t arrivals = last && !(kb & 1) ? 2 : 1;   // for the block that its step lacks, too
       kb += kSets;
       if (kb >= a.nk_l) settle();
       if (tile < tiles) load_scales();   // of this warp's next block, in flight meanwhile
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tcx::tmem_st_wait();
       tcx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_cluster(lead_bar(B_A_FULL + (n & 1)), arrivals);
+      if (lane == 0) arrive_cluster(lead_bar(B_A_FULL + (n & 1)));
     }
   } else if (warp >= kEpilogue0) {
     // ---- epilogue ----
@@ -456,7 +456,7 @@ int gemm_tc(const bf16* x, const Weights& w, bf16* out, int64_t M, int64_t N, in
   if (p_tiles * a.q_tiles >= (int64_t(1) << 31)) return set_error(QW_ERR_SHAPE, "qw_w4_gemm: too many output tiles");
   a.p_tiles = int(p_tiles);
   a.shards = shards;
-  a.nk_l = int((K_l + 63) / 64);
+  a.nk_l = int((K_l + 127) / 128) * 2;
   CUtensorMap mx, mc;
   const uint64_t xd[3] = {uint64_t(K_l), uint64_t(shards), uint64_t(M)}, xst[2] = {uint64_t(K_l) * 2, uint64_t(K) * 2};
   const uint32_t xb[3] = {64, 1, uint32_t(a.bn / 2)};

@@ -209,6 +209,9 @@ SHAPES = [
     (64, 515, 1024, 64, 1, COL, NONE), (65, 130, 224, 32, 1, COL, NONE), (127, 384, 512, 128, 2, ROW, NONE),
     (130, 272, 640, 64, 1, COL, SILU), (200, 1001, 288, 32, 3, ROW, NONE), (300, 640, 1152, 128, 2, COL, SILU),
     (257, 129, 96, 32, 1, COL, NONE), (513, 768, 2048, 128, 4, COL, NONE), (1000, 1024, 96, 32, 1, COL, SILU),
+    # more tiles than pairs of SMs, and K (or its shards) that ends inside 128 columns, or is shorter
+    (1999, 3001, 320, 64, 1, COL, NONE), (1500, 2500, 320, 32, 10, ROW, NONE), (1500, 2500, 576, 64, 3, ROW, NONE),
+    (2100, 4096, 448, 64, 2, COL, SILU), (1200, 4000, 32, 32, 1, COL, NONE),
 ]
 
 
