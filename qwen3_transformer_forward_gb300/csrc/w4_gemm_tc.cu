@@ -6,6 +6,7 @@
 // 128 of them and holds half of the tokens, so that the tokens cross L2 and each shared
 // memory once for 256 rows.
 #include <algorithm>
+#include <type_traits>
 
 #include "tc_common.cuh"
 #include "w4.cuh"
@@ -16,21 +17,26 @@ namespace w4 {
 __device__ unsigned int g_w4_error = 0;
 
 constexpr int kRows = 128;          // weight rows of a CTA (SiluAndMul: 64 gate rows and their up rows), two CTAs a tile
-constexpr int kMaxTokens = 192;     // tokens of a tile: two accumulators and four stages of A fill TMEM
-constexpr int XS = 4, CS = 4, AS = 4;   // stages: tokens (128 columns), codes (256), decoded weights (64, two a step)
-constexpr int kSets = 4;            // sets of four decoding warps, which take the 64-column blocks in turn
-// A set's next block lies kSets on and waits for the MMAs of the block AS before that one.  With kSets <= AS it is
-// among those that the set's last block waited for, or that block itself, so a parity is never two phases old.
-static_assert(kSets <= AS && AS == 4, "");
-constexpr int kDecode0 = 4, kEpilogue0 = kDecode0 + 4 * kSets, kThreads = 32 * (kEpilogue0 + 4);
-constexpr uint32_t X_HALF = kMaxTokens / 2 * 128, X_BYTES = 2 * X_HALF, C_BYTES = kRows * 128;
-constexpr uint32_t OFF_X = 0, OFF_C = XS * X_BYTES, OFF_BAR = OFF_C + CS * C_BYTES;
-constexpr size_t kTcSmem = 1024 + OFF_BAR + 512;
-constexpr uint32_t kTmemCols = 512, kTmemA = 2 * kMaxTokens;
-constexpr int B_X_FULL = 0, B_X_EMPTY = B_X_FULL + XS, B_C_FULL = B_X_EMPTY + XS, B_C_EMPTY = B_C_FULL + CS,
-              B_A_FULL = B_C_EMPTY + CS, B_A_EMPTY = B_A_FULL + AS / 2, B_ACC_FULL = B_A_EMPTY + AS, B_ACC_EMPTY = B_ACC_FULL + 2,
-              B_DRAIN = B_ACC_EMPTY + 2, N_BARS = B_DRAIN + 1;
-static_assert(N_BARS * 8 + 8 <= 512, "barrier area");
+// K advances in steps of 128 columns.  Stages: tokens (a step), codes (two), decoded weights (a step).  TMEM holds two
+// accumulators and the decoded weights.
+template <bool NARROW> struct Tile {
+  static constexpr int TOKENS = NARROW ? 128 : 192, XS = NARROW ? 5 : 4, CS = 4, AS = NARROW ? 4 : 2;
+  static constexpr int SETS = NARROW ? 3 : 2;   // sets of four decoding warps, which take the steps in turn
+  // A set's next step lies SETS on and waits for the MMAs of the step AS before that one.  With SETS <= AS it is among
+  // those that the set's last step waited for, or that step itself, so a parity is never two phases old.
+  static_assert(SETS <= AS, "");
+  static constexpr int EPILOGUE0 = 4 + 4 * SETS, THREADS = 32 * (EPILOGUE0 + 4);
+  static constexpr uint32_t X_HALF = TOKENS / 2 * 128, X_BYTES = 2 * X_HALF, C_BYTES = kRows * 128;
+  static constexpr uint32_t OFF_X = 0, OFF_C = XS * X_BYTES, OFF_BAR = OFF_C + CS * C_BYTES;
+  static constexpr size_t SMEM = 1024 + OFF_BAR + 512;
+  static constexpr uint32_t A = 2 * TOKENS;   // TMEM column of the decoded weights
+  static_assert(A + 64 * AS <= 512, "");
+  static constexpr int B_X_FULL = 0, B_X_EMPTY = B_X_FULL + XS, B_C_FULL = B_X_EMPTY + XS, B_C_EMPTY = B_C_FULL + CS,
+                       B_A_FULL = B_C_EMPTY + CS, B_A_EMPTY = B_A_FULL + AS, B_ACC_FULL = B_A_EMPTY + AS,
+                       B_ACC_EMPTY = B_ACC_FULL + 2, B_DRAIN = B_ACC_EMPTY + 2, N_BARS = B_DRAIN + 1;
+  static_assert(N_BARS * 8 + 8 <= 512, "barrier area");
+};
+constexpr uint32_t kTmemCols = 512;
 
 struct TcArgs {
   bf16* out;
@@ -39,7 +45,7 @@ struct TcArgs {
   int M, bn;              // tokens, tokens of a tile
   int p_tiles, q_tiles;   // weight row tiles, token tiles
   int shard_tiles;        // SiluAndMul: row tiles of a shard
-  int shards, nk_l;       // shards of K, 64-column blocks of a shard (even: a last one may hold zeros)
+  int shards, steps_l;    // shards of K, steps of 128 columns of a shard (the last may end in zeros)
 };
 
 // The two CTAs of a pair: rank 0 issues the MMAs and holds the barriers that both feed.
@@ -60,15 +66,6 @@ __device__ __forceinline__ void umma_ts(uint32_t lead, uint32_t d, uint32_t a, u
       " @q tcgen05.mma.cta_group::2.kind::f16 [%1], [%2], y, %5, p;\n}\n" ::"r"(lead),
       "r"(d), "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
       : "memory");
-}
-__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {   // without the wait
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t r;
@@ -116,13 +113,15 @@ __device__ __forceinline__ void tmem_ld32_arrived(uint32_t taddr, uint32_t (&r)[
       : "memory");
 }
 
-template <bool SILU, int GS>   // GS: log2 of a group's pieces of 32 columns
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool SILU, int GS, bool NARROW>   // GS: log2 of a group's pieces of 32 columns
+__global__ void __launch_bounds__(Tile<NARROW>::THREADS, 1)
     gemm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_c, TcArgs a) {
+  using T = Tile<NARROW>;
+  constexpr int XS = T::XS, CS = T::CS, AS = T::AS;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
-  const uint32_t sx = smem_u32(sm + OFF_X), sc = smem_u32(sm + OFF_C), bars = smem_u32(sm + OFF_BAR);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + OFF_BAR + N_BARS * 8);
+  const uint32_t sx = smem_u32(sm + T::OFF_X), sc = smem_u32(sm + T::OFF_C), bars = smem_u32(sm + T::OFF_BAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + T::OFF_BAR + T::N_BARS * 8);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   auto bar = [&](int b) { return bars + uint32_t(b) * 8u; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -130,12 +129,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto lead_bar = [&](int b) { return map_to_rank(bar(b), 0); };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < XS; ++i) tcx::mbar_init(bar(B_X_FULL + i), 1), tcx::mbar_init(bar(B_X_EMPTY + i), 1);
-    for (int i = 0; i < CS; ++i) tcx::mbar_init(bar(B_C_FULL + i), 1), tcx::mbar_init(bar(B_C_EMPTY + i), 16);
-    for (int i = 0; i < AS; ++i) tcx::mbar_init(bar(B_A_EMPTY + i), 1);
-    for (int i = 0; i < AS / 2; ++i) tcx::mbar_init(bar(B_A_FULL + i), 16);
-    for (int i = 0; i < 2; ++i) tcx::mbar_init(bar(B_ACC_FULL + i), 1), tcx::mbar_init(bar(B_ACC_EMPTY + i), 8);
-    tcx::mbar_init(bar(B_DRAIN), 1);
+    for (int i = 0; i < XS; ++i) tcx::mbar_init(bar(T::B_X_FULL + i), 1), tcx::mbar_init(bar(T::B_X_EMPTY + i), 1);
+    for (int i = 0; i < CS; ++i) tcx::mbar_init(bar(T::B_C_FULL + i), 1), tcx::mbar_init(bar(T::B_C_EMPTY + i), 8);
+    for (int i = 0; i < AS; ++i) tcx::mbar_init(bar(T::B_A_FULL + i), 8), tcx::mbar_init(bar(T::B_A_EMPTY + i), 1);
+    for (int i = 0; i < 2; ++i) tcx::mbar_init(bar(T::B_ACC_FULL + i), 1), tcx::mbar_init(bar(T::B_ACC_EMPTY + i), 8);
+    tcx::mbar_init(bar(T::B_DRAIN), 1);
     *abort_flag = 0;
     tcx::fence_mbar_init();
     tcx::prefetch_map(&tm_x);
@@ -166,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return true;
   };
-  const int tiles = a.p_tiles * a.q_tiles, ncs_l = (a.nk_l + 3) / 4;
+  const int tiles = a.p_tiles * a.q_tiles, ncs_l = (a.steps_l + 1) / 2;
   // first weight row (gate row) of a row tile; the stored rows of shard r of K begin at r * rows
   auto tile_row = [&](int p) -> int64_t {
     if (!SILU) return (int64_t(p) * 2 + rank) * kRows;
@@ -183,17 +181,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int tile = pair; tile < tiles && ok; tile += pairs) {
       const int m0 = tile / a.p_tiles * a.bn + rank * (a.bn / 2);
       for (int r = 0; r < a.shards && ok; ++r)
-        for (int kb = 0; kb < a.nk_l; kb += 2, ++n) {
-          const uint32_t s = n % XS, dst = sx + s * X_BYTES;
-          ok = wait(B_X_EMPTY + s, ((n / XS) & 1) ^ 1, 2u);
+        for (int k = 0; k < a.steps_l; ++k, ++n) {
+          const uint32_t s = n % XS, dst = sx + s * T::X_BYTES;
+          ok = wait(T::B_X_EMPTY + s, ((n / XS) & 1) ^ 1, 2u);
           if (!ok) break;
-          if (rank == 0) expect_tx(lead, bar(B_X_FULL + s), uint32_t(a.bn) * 256u);   // both CTAs' halves
-          tma_load_pair(lead, dst, &tm_x, lead_bar(B_X_FULL + s), kb * 64, r, m0);
-          tma_load_pair(lead, dst + X_HALF, &tm_x, lead_bar(B_X_FULL + s), kb * 64 + 64, r, m0);
+          if (rank == 0) expect_tx(lead, bar(T::B_X_FULL + s), uint32_t(a.bn) * 256u);   // both CTAs' halves
+          tma_load_pair(lead, dst, &tm_x, lead_bar(T::B_X_FULL + s), k * 128, r, m0);
+          tma_load_pair(lead, dst + T::X_HALF, &tm_x, lead_bar(T::B_X_FULL + s), k * 128 + 64, r, m0);
         }
     }
     if (!ok && rank == 0)   // the copies in flight land before the block ends
-      for (uint32_t i = n > XS ? n - XS : 0; i < n; ++i) tcx::mbar_wait(bar(B_X_FULL + i % XS), (i / XS) & 1, &g_w4_error, 2u);
+      for (uint32_t i = n > XS ? n - XS : 0; i < n; ++i) tcx::mbar_wait(bar(T::B_X_FULL + i % XS), (i / XS) & 1, &g_w4_error, 2u);
   } else if (warp == 2) {
     // ---- codes: 256 columns of this CTA's rows at a time ----
     const uint32_t lead = elect_one();
@@ -203,16 +201,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = int(tile_row(tile % a.p_tiles));
       for (int r = 0; r < a.shards && ok; ++r)
         for (int c = 0; c < ncs_l; ++c, ++n) {
-          const uint32_t s = n % CS, dst = sc + s * C_BYTES;
-          ok = wait(B_C_EMPTY + s, ((n / CS) & 1) ^ 1, 1u);
+          const uint32_t s = n % CS, dst = sc + s * T::C_BYTES;
+          ok = wait(T::B_C_EMPTY + s, ((n / CS) & 1) ^ 1, 1u);
           if (!ok) break;
-          expect_tx(lead, bar(B_C_FULL + s), C_BYTES);
-          tma_load(lead, dst, &tm_c, bar(B_C_FULL + s), c * 64, row, r);
-          if (SILU) tma_load(lead, dst + C_BYTES / 2, &tm_c, bar(B_C_FULL + s), c * 64, row + int(a.i_l), r);
+          expect_tx(lead, bar(T::B_C_FULL + s), T::C_BYTES);
+          tma_load(lead, dst, &tm_c, bar(T::B_C_FULL + s), c * 64, row, r);
+          if (SILU) tma_load(lead, dst + T::C_BYTES / 2, &tm_c, bar(T::B_C_FULL + s), c * 64, row + int(a.i_l), r);
         }
     }
     if (!ok)
-      for (uint32_t i = n > CS ? n - CS : 0; i < n; ++i) tcx::mbar_wait(bar(B_C_FULL + i % CS), (i / CS) & 1, &g_w4_error, 1u);
+      for (uint32_t i = n > CS ? n - CS : 0; i < n; ++i) tcx::mbar_wait(bar(T::B_C_FULL + i % CS), (i / CS) & 1, &g_w4_error, 1u);
   } else if (warp == 1) {
     if (rank == 0) {
       // ---- MMA, for both CTAs ----
@@ -220,135 +218,126 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc = tcx::idesc_bf16(2 * kRows, a.bn);
       const uint64_t desc = tcx::sw128_desc(sx);
       const uint32_t b_lo = uint32_t(desc), b_hi = uint32_t(desc >> 32);
-      uint32_t n = 0, u = 0;           // n: steps of two blocks
-      bool ok = true, ready = false;   // ready: this step's operands were seen there while the one before was issued
+      uint32_t n = 0, u = 0;
+      bool ok = true;
       for (int tile = pair; tile < tiles && ok; tile += pairs, ++u) {
-        const uint32_t d = tmem + (u & 1) * kMaxTokens;
+        const uint32_t d = tmem + (u & 1) * T::TOKENS;
         uint32_t add = 0;
-        ok = wait(B_ACC_EMPTY + (u & 1), ((u >> 1) & 1) ^ 1, 4u);
+        ok = wait(T::B_ACC_EMPTY + (u & 1), ((u >> 1) & 1) ^ 1, 4u);
         for (int r = 0; r < a.shards && ok; ++r)
-          for (int kb = 0; kb < a.nk_l; kb += 2, ++n) {
-            const uint32_t s = n % XS, h = n & 1;
-            if (!ready) ok = wait(B_X_FULL + s, (n / XS) & 1, 8u) && wait(B_A_FULL + h, (n >> 1) & 1, 16u);
+          for (int i = 0; i < a.steps_l; ++i, ++n) {
+            const uint32_t s = n % XS, h = n % AS;
+            ok = wait(T::B_X_FULL + s, (n / XS) & 1, 8u) && wait(T::B_A_FULL + h, (n / AS) & 1, 16u);
             if (!ok) break;
             tcx::tc_fence_after();
-            const uint32_t n1 = n + 1;
-            const bool x1 = test_wait(bar(B_X_FULL + n1 % XS), (n1 / XS) & 1), a1 = test_wait(bar(B_A_FULL + (n1 & 1)), (n1 >> 1) & 1);
-            const uint32_t b = b_lo + s * (X_BYTES >> 4), at = tmem + kTmemA + h * 64;
+            const uint32_t b = b_lo + s * (T::X_BYTES >> 4), at = tmem + T::A + h * 64;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              umma_ts(lead, d, at + k * 8, b + 2 * k, b_hi, idesc, add);
+            for (int k = 0; k < 8; ++k) {
+              umma_ts(lead, d, at + k * 8, b + (k >> 2) * (T::X_HALF >> 4) + 2 * (k & 3), b_hi, idesc, add);
               add = 1;
             }
-            umma_commit_pair(lead, bar(B_A_EMPTY + 2 * h));
-#pragma unroll
-            for (int k = 0; k < 4; ++k) umma_ts(lead, d, at + 32 + k * 8, b + (X_HALF >> 4) + 2 * k, b_hi, idesc, 1u);
-            umma_commit_pair(lead, bar(B_A_EMPTY + 2 * h + 1));
-            umma_commit_pair(lead, bar(B_X_EMPTY + s));
-            ready = x1 && a1;
+            umma_commit_pair(lead, bar(T::B_A_EMPTY + h));
+            umma_commit_pair(lead, bar(T::B_X_EMPTY + s));
           }
-        if (ok) umma_commit_pair(lead, bar(B_ACC_FULL + (u & 1)));
+        if (ok) umma_commit_pair(lead, bar(T::B_ACC_FULL + (u & 1)));
       }
-      umma_commit_pair(lead, bar(B_DRAIN));
-      tcx::mbar_wait(bar(B_DRAIN), 0, &g_w4_error, 32u);
+      umma_commit_pair(lead, bar(T::B_DRAIN));
+      tcx::mbar_wait(bar(T::B_DRAIN), 0, &g_w4_error, 32u);
     }
-  } else if (warp >= kDecode0 && warp < kEpilogue0) {
-    // ---- decode: one weight row a thread, four warps the rows of a block of 64 columns ----
-    const int q = warp & 3, set = (warp - kDecode0) >> 2;
+  } else if (warp >= 4 && warp < T::EPILOGUE0) {
+    // ---- decode: one weight row a thread, four warps the rows of a step ----
+    const int q = warp & 3, set = (warp - 4) >> 2;
     const int srow = SILU ? (lane >> 4) * 64 + 16 * q + (lane & 15) : 32 * q + lane;   // row in the code stage
     const int64_t row_off = SILU ? (lane >> 4) * a.i_l + 16 * q + (lane & 15) : srow;
-    const uint32_t code_row = sc + uint32_t(srow) * 128u, tmem_row = tmem + (uint32_t(32 * q) << 16) + kTmemA;
+    const uint32_t code_row = sc + uint32_t(srow) * 128u, tmem_row = tmem + (uint32_t(32 * q) << 16) + T::A;
     const uint16_t* scales = reinterpret_cast<const uint16_t*>(a.w.scales);
-    // the block: its tile, shard r of K, place kb in the shard; cs0, n0: code stages and MMA steps before this shard
-    int tile = pair, r = 0, kb = set;
-    uint32_t cs0 = 0, n0 = 0;
-    const uint16_t* sp = nullptr;   // scales (and offset of the zeros) of this thread's row in the block's shard
-    int64_t zo = 0;
+    // the step: number n, its tile, shard r of K, place k in the shard; cs0: code stages before this shard
+    int tile = pair, r = 0, k = set;
+    uint32_t n = set, cs0 = 0;
+    const uint16_t* sp = nullptr;   // scales and zeros of this thread's row in the step's shard
+    const uint8_t* zp = nullptr;
     bool have = false;
-    auto settle = [&]() {   // kb may lie past its shard
-      while (kb >= a.nk_l) {
-        kb -= a.nk_l;
+    auto settle = [&]() {   // k may lie past its shard
+      while (k >= a.steps_l) {
+        k -= a.steps_l;
         cs0 += ncs_l;
-        n0 += a.nk_l / 2;
         if (++r == a.shards) {
           r = 0;
           tile += pairs;
         }
       }
       if (tile >= tiles) return;
-      const int64_t row = tile_row(tile % a.p_tiles) + row_off;
+      const int64_t row = tile_row(tile % a.p_tiles) + row_off, at = (int64_t(r) * a.rows + row) * a.w.groups;
       have = row < a.rows;
-      zo = (int64_t(r) * a.rows + row) * a.w.groups;
-      sp = scales + zo;
+      sp = scales + at;
+      zp = a.w.zeros != nullptr ? a.w.zeros + at : nullptr;
     };
-    // scale and zero point of the block's two pieces of 32 columns, the scale 0 where there is none
-    uint32_t s[2], z[2];
+    // scales and zero points of the step's groups, the scale 0 where there is none
+    constexpr int NG = 4 >> GS;
+    uint32_t s[NG], z[NG];
     auto load_scales = [&]() {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (GS > 0 && e == 1) {   // one group
-          s[1] = s[0];
-          z[1] = z[0];
-          break;
-        }
-        const int g = (2 * kb + e) >> GS;
+      for (int e = 0; e < NG; ++e) {
+        const int g = k * NG + e;
         const bool in = have && g < a.w.groups;
         s[e] = in ? __ldg(sp + g) : 0u;
-        z[e] = in && a.w.zeros != nullptr ? __ldg(a.w.zeros + zo + g) : 8u;
+        z[e] = in && zp != nullptr ? __ldg(zp + g) : 8u;
       }
     };
     settle();
     if (tile < tiles) load_scales();
     while (tile < tiles) {
-      const uint32_t cs = cs0 + uint32_t(kb >> 2), st = cs % CS, in_stage = uint32_t(kb & 3);
-      const uint32_t n = n0 + uint32_t(kb >> 1), slot = 2 * (n & 1) + uint32_t(kb & 1), a_parity = ((n >> 1) & 1) ^ 1;
-      const bool last = kb == a.nk_l - 1;
-      const uint32_t s2[2] = {scale_pair(s[0]), scale_pair(s[1])}, z2[2] = {offset_pair(z[0]), offset_pair(z[1])};
-      kb += kSets;
-      if (kb >= a.nk_l) settle();
-      if (tile < tiles) load_scales();   // of this warp's next block, in flight meanwhile
-      if (!__all_sync(0xffffffffu, wait(B_C_FULL + st, (cs / CS) & 1, 64u))) break;   // the warp goes on as one
-      uint4 v[2];
+      const uint32_t cs = cs0 + uint32_t(k >> 1), st = cs % CS, in_stage = uint32_t(k & 1);
+      const uint32_t h = n % AS, a_parity = ((n / AS) & 1) ^ 1;
+      const uint32_t arrivals = k == a.steps_l - 1 && !in_stage ? 2u : 1u;   // for the step that its code stage lacks, too
+      uint32_t s2[NG], z2[NG];
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < NG; ++e) s2[e] = scale_pair(s[e]), z2[e] = offset_pair(z[e]);
+      n += T::SETS;
+      k += T::SETS;
+      if (k >= a.steps_l) settle();
+      if (tile < tiles) load_scales();   // of this warp's next step, in flight meanwhile
+      if (!__all_sync(0xffffffffu, wait(T::B_C_FULL + st, (cs / CS) & 1, 64u))) break;   // the warp goes on as one
+      uint4 v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(v[e].x), "=r"(v[e].y), "=r"(v[e].z), "=r"(v[e].w)
-                     : "r"(code_row + st * C_BYTES + (((2 * in_stage + e) ^ uint32_t(srow & 7)) << 4)));
-      uint32_t w[32];
+                     : "r"(code_row + st * T::C_BYTES + (((4 * in_stage + e) ^ uint32_t(srow & 7)) << 4)));
+      uint32_t w[2][32];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < 4; ++e) {
         const uint32_t word[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t o[4];
-          decode(word[i], z2[e], s2[e], o);
+          decode(word[i], z2[e >> GS], s2[e >> GS], o);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) w[16 * e + 4 * i + k] = o[k];
+          for (int j = 0; j < 4; ++j) w[e >> 1][16 * (e & 1) + 4 * i + j] = o[j];
         }
       }
       __syncwarp();
-      // a stage is free after 16 arrivals: of the four warps of each of its blocks, the last block's for those it lacks
-      if (lane == 0)
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar(B_C_EMPTY + st)), "r"(last ? 4u - in_stage : 1u)
-                     : "memory");
-      if (!__all_sync(0xffffffffu, wait(B_A_EMPTY + slot, a_parity, 128u))) break;
+      if (lane == 0)   // a stage is free after 8 arrivals: of the four warps of each of its two steps
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar(T::B_C_EMPTY + st)), "r"(arrivals) : "memory");
+      if (!__all_sync(0xffffffffu, wait(T::B_A_EMPTY + h, a_parity, 128u))) break;
       tcx::tc_fence_after();
-      tcx::tmem_st32(tmem_row + slot * 32, w);
+      tcx::tmem_st32(tmem_row + h * 64, w[0]);
+      tcx::tmem_st32(tmem_row + h * 64 + 32, w[1]);
       tcx::tmem_st_wait();
       tcx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_cluster(lead_bar(B_A_FULL + (n & 1)));
+      if (lane == 0) arrive_cluster(lead_bar(T::B_A_FULL + h));
     }
-  } else if (warp >= kEpilogue0) {
+  } else if (warp >= T::EPILOGUE0) {
     // ---- epilogue ----
     const int q = warp & 3;
     const bool even = (a.ldc & 1) == 0;   // two outputs of a token make an aligned word
     uint32_t u = 0;
     for (int tile = pair; tile < tiles; tile += pairs, ++u) {
-      if (!__all_sync(0xffffffffu, wait(B_ACC_FULL + (u & 1), (u >> 1) & 1, 256u))) break;
+      if (!__all_sync(0xffffffffu, wait(T::B_ACC_FULL + (u & 1), (u >> 1) & 1, 256u))) break;
       tcx::tc_fence_after();
       const int p = tile % a.p_tiles, m0 = tile / a.p_tiles * a.bn, m1 = min(m0 + a.bn, a.M);
-      const uint32_t d = tmem + (uint32_t(32 * q) << 16) + (u & 1) * kMaxTokens;
+      const uint32_t d = tmem + (uint32_t(32 * q) << 16) + (u & 1) * T::TOKENS;
       int64_t o;       // output column of this thread
       bool have;
       if (SILU) {
@@ -366,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c + 32 >= a.bn) {   // the accumulator is read out
           tcx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive_cluster(lead_bar(B_ACC_EMPTY + (u & 1)));
+          if (lane == 0) arrive_cluster(lead_bar(T::B_ACC_EMPTY + (u & 1)));
         }
         const int left = m1 - m0 - c;   // tokens of these columns
         if (SILU) {
@@ -412,17 +401,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool SILU, int GS>
+template <bool SILU, int GS, bool NARROW>
 static int launch(const CUtensorMap& mx, const CUtensorMap& mc, const TcArgs& a, cudaStream_t st) {
-  auto kern = gemm_tc_kernel<SILU, GS>;
+  auto kern = gemm_tc_kernel<SILU, GS, NARROW>;
   static const cudaError_t set =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kTcSmem));
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Tile<NARROW>::SMEM));
   if (set != cudaSuccess) return set_error(QW_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(set));
   const int tiles = a.p_tiles * a.q_tiles;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(2 * std::min(tiles, 76)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kTcSmem;
+  cfg.blockDim = dim3(Tile<NARROW>::THREADS);
+  cfg.dynamicSmemBytes = Tile<NARROW>::SMEM;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -448,7 +437,7 @@ int gemm_tc(const bf16* x, const Weights& w, bf16* out, int64_t M, int64_t N, in
   a.ldc = silu ? N / 2 : N;
   a.i_l = silu ? N / 2 / tp : 0;
   a.M = int(M);
-  a.q_tiles = int((M + kMaxTokens - 1) / kMaxTokens);
+  a.q_tiles = int((M + Tile<false>::TOKENS - 1) / Tile<false>::TOKENS);
   a.bn = int((M + a.q_tiles - 1) / a.q_tiles + 15) / 16 * 16;
   a.q_tiles = int((M + a.bn - 1) / a.bn);
   a.shard_tiles = silu ? int((a.i_l + kRows - 1) / kRows) : 0;
@@ -456,7 +445,7 @@ int gemm_tc(const bf16* x, const Weights& w, bf16* out, int64_t M, int64_t N, in
   if (p_tiles * a.q_tiles >= (int64_t(1) << 31)) return set_error(QW_ERR_SHAPE, "qw_w4_gemm: too many output tiles");
   a.p_tiles = int(p_tiles);
   a.shards = shards;
-  a.nk_l = int((K_l + 127) / 128) * 2;
+  a.steps_l = int((K_l + 127) / 128);
   CUtensorMap mx, mc;
   const uint64_t xd[3] = {uint64_t(K_l), uint64_t(shards), uint64_t(M)}, xst[2] = {uint64_t(K_l) * 2, uint64_t(K) * 2};
   const uint32_t xb[3] = {64, 1, uint32_t(a.bn / 2)};
@@ -468,11 +457,13 @@ int gemm_tc(const bf16* x, const Weights& w, bf16* out, int64_t M, int64_t N, in
   const uint32_t cb[3] = {64, silu ? 64u : 128u, 1};
   rc = make_tensor_map(&mc, w.codes, 3, cd, cst, cb);
   if (rc) return rc;
-  switch (w.group_shift) {
-    case 0: return silu ? launch<true, 0>(mx, mc, a, st) : launch<false, 0>(mx, mc, a, st);
-    case 1: return silu ? launch<true, 1>(mx, mc, a, st) : launch<false, 1>(mx, mc, a, st);
-    default: return silu ? launch<true, 2>(mx, mc, a, st) : launch<false, 2>(mx, mc, a, st);
-  }
+  const int gs = w.group_shift;
+  auto go = [&](auto narrow) {
+    constexpr bool NA = decltype(narrow)::value;
+    if (silu) return gs == 0 ? launch<true, 0, NA>(mx, mc, a, st) : gs == 1 ? launch<true, 1, NA>(mx, mc, a, st) : launch<true, 2, NA>(mx, mc, a, st);
+    return gs == 0 ? launch<false, 0, NA>(mx, mc, a, st) : gs == 1 ? launch<false, 1, NA>(mx, mc, a, st) : launch<false, 2, NA>(mx, mc, a, st);
+  };
+  return a.bn <= Tile<true>::TOKENS ? go(std::true_type{}) : go(std::false_type{});
 }
 
 }  // namespace w4
