@@ -40,12 +40,22 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t offset_pair(uint32_t z) { return 0x43004300u + z * 0x00010001u; }
 __device__ __forceinline__ uint32_t scale_pair(uint32_t s_bits) { return s_bits * 0x00010001u; }
 
+// 0x43004300 in a register that the compiler takes for unknown: (x & mask) | magic is then one instruction, with two
+// constants it is two (25.9 -> 23.0 cycles a word on an SM sub-partition with the rest of decode).
+__device__ __forceinline__ uint32_t code_magic() {
+  uint32_t m;
+  asm volatile("mov.b32 %0, 0x43004300;" : "=r"(m));
+  return m;
+}
 // The 8 weights of a word as 4 bf16 pairs in column order: 128 + n by bit operations, less
 // 128 + z (exact), times the scale (rounded once: the weight's definition).
-__device__ __forceinline__ void decode(uint32_t word, uint32_t z2, uint32_t s2, uint32_t (&w)[4]) {
+__device__ __forceinline__ void decode(uint32_t word, uint32_t magic, uint32_t z2, uint32_t s2, uint32_t (&w)[4]) {
 #pragma unroll
-  for (int p = 0; p < 4; ++p)
-    w[p] = mul_bf16x2(sub_bf16x2(((word >> (4 * p)) & 0x000f000fu) | 0x43004300u, z2), s2);
+  for (int p = 0; p < 4; ++p) {
+    uint32_t v;
+    asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(v) : "r"(word >> (4 * p)), "r"(magic));   // (x & mask) | magic
+    w[p] = mul_bf16x2(sub_bf16x2(v, z2), s2);
+  }
 }
 
 }  // namespace w4

@@ -247,6 +247,7 @@ __global__ void __launch_bounds__(Tile<NARROW>::THREADS, 1)
   } else if (warp >= 4 && warp < T::EPILOGUE0) {
     // ---- decode: one weight row a thread, four warps the rows of a step ----
     const int q = warp & 3, set = (warp - 4) >> 2;
+    const uint32_t magic = code_magic();
     const int srow = SILU ? (lane >> 4) * 64 + 16 * q + (lane & 15) : 32 * q + lane;   // row in the code stage
     const int64_t row_off = SILU ? (lane >> 4) * a.i_l + 16 * q + (lane & 15) : srow;
     const uint32_t code_row = sc + uint32_t(srow) * 128u, tmem_row = tmem + (uint32_t(32 * q) << 16) + T::A;
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(Tile<NARROW>::THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t o[4];
-          decode(word[i], z2[e >> GS], s2[e >> GS], o);
+          decode(word[i], magic, z2[e >> GS], s2[e >> GS], o);
 #pragma unroll
           for (int j = 0; j < 4; ++j) w[e >> 1][16 * (e & 1) + 4 * i + j] = o[j];
         }

@@ -44,106 +44,201 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
 }
 
 constexpr int kWarps = 8;
+constexpr size_t gemv_smem(int nt, int r) { return size_t(kWarps) * 16 * r * (nt * 8 + 1) * 4; }
 
-// A warp takes a tile of 16 weight rows and every split-th chunk of 128 columns; lane (g, t) = (lane / 4,
+// A warp takes R tiles of 16 weight rows and every split-th chunk of 128 columns; lane (g, t) = (lane / 4,
 // lane % 4) holds the 32 columns of piece t of rows g and g + 8.  The k index of an MMA may be any
 // permutation that weights and tokens share, so a lane's own columns are its k values: no shuffles.
-template <int NT, bool SILU>
+// The codes of PF chunks are in flight at once, the first ones ahead of the programmatic wait.
+// WHOLE: a shard's columns are whole chunks, so that nothing in the loop has a condition of its own lane.
+template <int NT, int R, int PF, bool SILU, bool ZEROS, bool WHOLE>
 __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(GemvArgs a) {
-  __shared__ float red[kWarps][16][NT * 8 + 1];
+  extern __shared__ float red_dyn[];   // [kWarps][16 R][NT * 8 + 1]
+  float(*red)[16 * R][NT * 8 + 1] = reinterpret_cast<float(*)[16 * R][NT * 8 + 1]>(red_dyn);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int per_cta = kWarps / a.split, sl = warp % a.split;
-  const int64_t tile0 = int64_t(blockIdx.x) * per_cta, tile = tile0 + warp / a.split;
+  const int64_t tile0 = int64_t(blockIdx.x) * per_cta * R, tile = tile0 + warp / a.split * R;
   const int m0 = blockIdx.y * (NT * 8);
-  int64_t ra, rb;
-  bool oka = tile < a.tiles, okb = oka;
-  if (SILU) {
-    const int64_t o = tile * 8 + g, r = o / a.i_l;
-    ra = o + r * a.i_l;
-    rb = ra + a.i_l;
-  } else {
-    ra = tile * 16 + g;
-    rb = ra + 8;
-    oka = ra < a.rows;
-    okb = rb < a.rows;
-  }
-  float acc[NT][4];
+  const uint32_t magic = code_magic();
+  // this lane's piece within its shard, pieces from it to the end of K, pieces to the next one
+  int lu = 4 * sl + t, left = a.pieces - lu;
+  const int advance = 4 * a.split;
+  // rows g and g + 8 of each tile (SiluAndMul: gate and up of output g): codes and scales at the next piece.
+  // A row that is not there reads row 0 and is not stored.
+  const uint8_t* cp[R][2];
+  const uint16_t* sp[R][2];
+  const uint8_t* zp[R][2];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
+  for (int q = 0; q < R; ++q) {
+    int64_t row[2];
+    if (SILU) {
+      const int64_t o = (tile + q) * 8 + g, r = o / a.i_l;
+      row[0] = tile + q < a.tiles ? o + r * a.i_l : 0;
+      row[1] = tile + q < a.tiles ? row[0] + a.i_l : 0;
+    } else {
+      row[0] = (tile + q) * 16 + g;
+      row[1] = row[0] + 8;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (row[e] >= a.rows) row[e] = 0;
+      cp[q][e] = a.w.codes + row[e] * a.w.row_bytes + int64_t(lu) * 16;
+      sp[q][e] = reinterpret_cast<const uint16_t*>(a.w.scales) + row[e] * a.w.groups + (lu >> a.w.group_shift);
+      zp[q][e] = a.w.zeros + row[e] * a.w.groups + (lu >> a.w.group_shift);
+    }
+  }
+  const int64_t to_shard_c = (a.rows - 1) * a.w.row_bytes, to_shard_s = (a.rows - 1) * a.w.groups;
+  struct Chunk {
+    uint4 c[R][2];
+    uint32_t s[R][2], z[R][2];
+  };
+  Chunk buf[PF];
+  auto load = [&](Chunk& b) {
+    while (lu >= a.pieces_l && left > 0) {   // on to the next shard's rows
+      lu -= a.pieces_l;
+#pragma unroll
+      for (int q = 0; q < R; ++q)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          cp[q][e] += to_shard_c;
+          sp[q][e] += to_shard_s;
+          zp[q][e] += to_shard_s;
+        }
+    }
+    const int step = WHOLE ? advance >> a.w.group_shift
+                           : ((lu + advance) >> a.w.group_shift) - (lu >> a.w.group_shift);
+#pragma unroll
+    for (int q = 0; q < R; ++q)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (!WHOLE) {
+          b.c[q][e] = make_uint4(0, 0, 0, 0);
+          b.s[q][e] = 0;
+          b.z[q][e] = 8;
+        }
+        if (left > 0) {
+          b.c[q][e] = ldg_codes(cp[q][e]);
+          b.s[q][e] = __ldg(sp[q][e]);
+          if (ZEROS) b.z[q][e] = __ldg(zp[q][e]);
+        }
+        cp[q][e] += 16 * advance;
+        sp[q][e] += step;
+        if (ZEROS) zp[q][e] += step;
+      }
+    lu += advance;
+    left -= advance;
+  };
+  float acc[R][NT][4];
+#pragma unroll
+  for (int q = 0; q < R; ++q)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[q][n][0] = acc[q][n][1] = acc[q][n][2] = acc[q][n][3] = 0.0f;
+#pragma unroll
+  for (int d = 0; d < PF; ++d) load(buf[d]);
   pdl_wait();
   pdl_trigger();
-  int64_t shard = 0;           // first row of the shard's block
-  int ul = 4 * sl + t;         // piece within the shard
-  for (int u = ul; u - t < a.pieces; u += 4 * a.split, ul += 4 * a.split) {
-    while (ul >= a.pieces_l) {
-      ul -= a.pieces_l;
-      shard += a.rows;
-    }
-    const bool in = u < a.pieces;
-    uint4 ca = make_uint4(0, 0, 0, 0), cb = ca;
-    uint32_t sa = 0, sb = 0, za = 8, zb = 8;
-    const int grp = ul >> a.w.group_shift;
-    if (in && oka) {
-      ca = ldg_codes(a.w.codes + (shard + ra) * a.w.row_bytes + int64_t(ul) * 16);
-      sa = __ldg(reinterpret_cast<const uint16_t*>(a.w.scales) + (shard + ra) * a.w.groups + grp);
-      if (a.w.zeros != nullptr) za = __ldg(a.w.zeros + (shard + ra) * a.w.groups + grp);
-    }
-    if (in && okb) {
-      cb = ldg_codes(a.w.codes + (shard + rb) * a.w.row_bytes + int64_t(ul) * 16);
-      sb = __ldg(reinterpret_cast<const uint16_t*>(a.w.scales) + (shard + rb) * a.w.groups + grp);
-      if (a.w.zeros != nullptr) zb = __ldg(a.w.zeros + (shard + rb) * a.w.groups + grp);
-    }
-    const uint32_t sa2 = scale_pair(sa), sb2 = scale_pair(sb), za2 = offset_pair(za), zb2 = offset_pair(zb);
-    const uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t pa[4], pb[4];
-      decode(wa[i], za2, sa2, pa);
-      decode(wb[i], zb2, sb2, pb);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int tok = m0 + n * 8 + g;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (in && tok < a.M) x = __ldg(reinterpret_cast<const uint4*>(a.x + int64_t(tok) * a.K + u * kPiece + 8 * i));
-        mma_16816(acc[n], pa[0], pb[0], pa[1], pb[1], x.x, x.y);
-        mma_16816(acc[n], pa[2], pb[2], pa[3], pb[3], x.z, x.w);
-      }
-    }
-  }
+  // this lane's token of each group of 8; past the last one it is token 0, whose sums there are not stored
+  const bf16* xp[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    red[warp][g][n * 8 + 2 * t] = acc[n][0];
-    red[warp][g][n * 8 + 2 * t + 1] = acc[n][1];
-    red[warp][g + 8][n * 8 + 2 * t] = acc[n][2];
-    red[warp][g + 8][n * 8 + 2 * t + 1] = acc[n][3];
+    const int tok = m0 + n * 8 + g;
+    xp[n] = a.x + int64_t(tok < a.M ? tok : 0) * a.K + (4 * sl + t) * kPiece;
   }
+  for (int u0 = 4 * sl; u0 < a.pieces; u0 += advance * PF) {
+#pragma unroll
+    for (int d = 0; d < PF; ++d) {
+      const int u = u0 + advance * d;
+      if (u >= a.pieces) break;
+      const bool in = WHOLE || u + t < a.pieces;
+      uint4 x[4][NT];
+      auto load_x = [&](int i) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (!WHOLE) x[i][n] = make_uint4(0, 0, 0, 0);
+          if (in) x[i][n] = __ldg(reinterpret_cast<const uint4*>(xp[n] + 8 * i));
+        }
+      };
+      constexpr int AHEAD = NT <= 2 ? 4 : NT <= 6 ? 2 : 1;   // words of tokens in flight
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) load_x(i);
+      Chunk& b = buf[d];
+      uint32_t s2[R][2], z2[R][2];
+#pragma unroll
+      for (int q = 0; q < R; ++q)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) s2[q][e] = scale_pair(b.s[q][e]), z2[q][e] = offset_pair(ZEROS ? b.z[q][e] : 8u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+          uint32_t pa[4], pb[4];
+          const uint32_t wa = i == 0 ? b.c[q][0].x : i == 1 ? b.c[q][0].y : i == 2 ? b.c[q][0].z : b.c[q][0].w;
+          const uint32_t wb = i == 0 ? b.c[q][1].x : i == 1 ? b.c[q][1].y : i == 2 ? b.c[q][1].z : b.c[q][1].w;
+          decode(wa, magic, z2[q][0], s2[q][0], pa);
+          decode(wb, magic, z2[q][1], s2[q][1], pb);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_16816(acc[q][n], pa[0], pb[0], pa[1], pb[1], x[i][n].x, x[i][n].y);
+            mma_16816(acc[q][n], pa[2], pb[2], pa[3], pb[3], x[i][n].z, x[i][n].w);
+          }
+        }
+        if (i + AHEAD < 4) load_x(i + AHEAD);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) xp[n] += advance * kPiece;
+      load(b);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < R; ++q)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      red[warp][16 * q + g][n * 8 + 2 * t] = acc[q][n][0];
+      red[warp][16 * q + g][n * 8 + 2 * t + 1] = acc[q][n][1];
+      red[warp][16 * q + g + 8][n * 8 + 2 * t] = acc[q][n][2];
+      red[warp][16 * q + g + 8][n * 8 + 2 * t + 1] = acc[q][n][3];
+    }
   __syncthreads();
-  const int out_rows = SILU ? 8 : 16;
-  for (int e = threadIdx.x; e < per_cta * out_rows * NT * 8; e += kWarps * 32) {
-    const int r = e % out_rows, lt = e / out_rows % per_cta, n = e / (out_rows * per_cta);
+  constexpr int out_rows = SILU ? 8 : 16;   // of a tile
+  const int total = per_cta * R * out_rows, live = min(NT * 8, a.M - m0);
+  for (int e = threadIdx.x; e < total * live; e += kWarps * 32) {
+    const int j = e % total, n = e / total, lt = j / out_rows, r = j % out_rows;
     const int64_t o = (tile0 + lt) * out_rows + r;
-    if (m0 + n >= a.M || o >= (SILU ? a.rows / 2 : a.rows)) continue;
+    if (o >= (SILU ? a.rows / 2 : a.rows)) continue;
     float v = 0.0f, up = 0.0f;
     for (int s = 0; s < a.split; ++s) {   // in slice order
-      v += red[lt * a.split + s][r][n];
-      if (SILU) up += red[lt * a.split + s][r + 8][n];
+      const int w = lt / R * a.split + s, row = lt % R * 16 + r;
+      v += red[w][row][n];
+      if (SILU) up += red[w][row + 8][n];
     }
     if (SILU) v = __fdividef(v, 1.0f + __expf(-v)) * up;
     a.out[int64_t(m0 + n) * a.ldc + o] = __float2bfloat16_rn(v);
   }
 }
 
-template <int NT>
-static int launch_gemv(GemvArgs a, bool silu, cudaStream_t st) {
+template <int NT, int R, int PF, bool SILU, bool ZEROS, bool WHOLE>
+static int launch_gemv(GemvArgs a, cudaStream_t st) {
+  auto kern = gemv_kernel<NT, R, PF, SILU, ZEROS, WHOLE>;
+  constexpr size_t smem = gemv_smem(NT, R);
+  if (smem > 48 * 1024) {
+    static const cudaError_t set = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (set != cudaSuccess) return set_error(QW_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(set));
+  }
   const int chunks = (a.pieces + 3) / 4;
+  const int64_t units = (a.tiles + R - 1) / R;
   a.split = 8;
-  while (a.split > 1 && (a.split > chunks || a.tiles * a.split > 152 * 32)) a.split >>= 1;
+  while (a.split > 1 && (a.split > chunks || units * a.split > 152 * 32)) a.split >>= 1;
   const int per_cta = kWarps / a.split;
-  const dim3 grid(unsigned((a.tiles + per_cta - 1) / per_cta), unsigned((a.M + NT * 8 - 1) / (NT * 8)));
-  if (grid.y > 65535) return set_error(QW_ERR_SHAPE, "qw_w4_gemm: too many tokens");
-  if (silu) launch_pdl(gemv_kernel<NT, true>, grid, kWarps * 32, 0, st, a);
-  else launch_pdl(gemv_kernel<NT, false>, grid, kWarps * 32, 0, st, a);
+  const dim3 grid(unsigned((units + per_cta - 1) / per_cta), unsigned((a.M + NT * 8 - 1) / (NT * 8)));
+  launch_pdl(kern, grid, kWarps * 32, smem, st, a);
   return check_launch("w4 gemv");
+}
+
+template <int NT, int R, int PF, bool WHOLE>
+static int launch_gemv(const GemvArgs& a, bool silu, cudaStream_t st) {
+  if (a.w.zeros != nullptr)
+    return silu ? launch_gemv<NT, R, PF, true, true, WHOLE>(a, st) : launch_gemv<NT, R, PF, false, true, WHOLE>(a, st);
+  return silu ? launch_gemv<NT, R, PF, true, false, WHOLE>(a, st) : launch_gemv<NT, R, PF, false, false, WHOLE>(a, st);
 }
 
 static int linear(const bf16* x, const void* codes, const void* scales, const void* zeros, bf16* out, int64_t M, int64_t N,
@@ -163,10 +258,17 @@ static int linear(const bf16* x, const void* codes, const void* scales, const vo
   a.pieces = int(K / kPiece);
   a.pieces_l = int(K_l / kPiece);
   if (M > 64) return gemm_tc(x, a.w, out, M, N, K, mode == QW_GEMM_ROW_REDUCE ? tp : 1, tp, silu, st);
-  if (M <= 8) return launch_gemv<1>(a, silu, st);
-  if (M <= 16) return launch_gemv<2>(a, silu, st);
-  if (M <= 32) return launch_gemv<4>(a, silu, st);
-  return launch_gemv<8>(a, silu, st);
+  const int nt = int((M + 7) / 8);
+  if (a.pieces_l % 4) return nt <= 1 ? launch_gemv<1, 1, 2, false>(a, silu, st) : launch_gemv<4, 1, 1, false>(a, silu, st);
+  switch (nt) {
+    case 1: return launch_gemv<1, 1, 2, true>(a, silu, st);
+    case 2: return launch_gemv<2, 2, 2, true>(a, silu, st);
+    case 3: return launch_gemv<3, 2, 2, true>(a, silu, st);
+    case 4: return launch_gemv<4, 2, 2, true>(a, silu, st);
+    case 5: return launch_gemv<5, 2, 2, true>(a, silu, st);
+    case 6: return launch_gemv<6, 2, 2, true>(a, silu, st);
+    default: return launch_gemv<8, 2, 1, true>(a, silu, st);
+  }
 }
 
 // argmax over rows of bf16 logits of any width, lowest index on ties (as qw_argmax; NaN is passed over)

@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(256) embed_kernel(const int64_t* __restrict__ 
     const int k = first + 32 * i;
     if (k >= words) break;
     uint32_t w[4];
-    decode(c[i], offset_pair(z[i]), scale_pair(s[i]), w);
+    decode(c[i], code_magic(), offset_pair(z[i]), scale_pair(s[i]), w);
     if (!ok) w[0] = w[1] = w[2] = w[3] = 0;   // (0 - z) * 0 is a negative zero
     reinterpret_cast<uint4*>(out + tok * H)[k] = make_uint4(w[0], w[1], w[2], w[3]);
   }
