@@ -37,6 +37,7 @@ template <bool NARROW> struct Tile {
   static_assert(N_BARS * 8 + 8 <= 512, "barrier area");
 };
 constexpr uint32_t kTmemCols = 512;
+constexpr int kPairs = 76;          // of 152 SMs
 
 struct TcArgs {
   bf16* out;
@@ -46,16 +47,17 @@ struct TcArgs {
   int p_tiles, q_tiles;   // weight row tiles, token tiles
   int shard_tiles;        // SiluAndMul: row tiles of a shard
   int shards, steps_l;    // shards of K, steps of 128 columns of a shard (the last may end in zeros)
+  int splits;             // pairs that share a tile's K (a cluster, one tile each); 1: every pair walks over tiles
 };
 
 // The two CTAs of a pair: rank 0 issues the MMAs and holds the barriers that both feed.
 // Issued by the lane with `lead`, as a predicate: the warp stays converged and its operands in uniform registers (61 ->
 // 20 cycles an MMA, 110 -> 22 a commit, against one lane in a branch).
-__device__ __forceinline__ void umma_commit_pair(uint32_t lead, uint32_t bar) {   // arrives at this offset in both CTAs
+__device__ __forceinline__ void umma_commit_pair(uint32_t lead, uint32_t bar, uint32_t mask) {   // at this offset in the CTAs of mask
   asm volatile(
       "{\n .reg .pred q;\n setp.ne.b32 q, %0, 0;\n"
       " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%1], %2;\n}\n" ::"r"(lead),
-      "r"(bar), "h"(uint16_t(3))
+      "r"(bar), "h"(uint16_t(mask))
       : "memory");
 }
 // B descriptors come as their low word and a constant high word
@@ -125,8 +127,11 @@ __global__ void __launch_bounds__(Tile<NARROW>::THREADS, 1)
   volatile uint32_t* abort_flag = tmem_slot + 1;
   auto bar = [&](int b) { return bars + uint32_t(b) * 8u; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = int(cluster_rank()), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  auto lead_bar = [&](int b) { return map_to_rank(bar(b), 0); };
+  // rank 0 of the pair leads it; the pairs of a cluster share one tile's K
+  const uint32_t crank = cluster_rank(), lead_rank = crank & ~1u, both = 3u << lead_rank;
+  const int rank = int(crank & 1), split = int(crank >> 1);
+  const int pair = blockIdx.x / (2 * a.splits), pairs = gridDim.x / (2 * a.splits);
+  auto lead_bar = [&](int b) { return map_to_rank(bar(b), lead_rank); };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < XS; ++i) tcx::mbar_init(bar(T::B_X_FULL + i), 1), tcx::mbar_init(bar(T::B_X_EMPTY + i), 1);
@@ -165,6 +170,12 @@ __global__ void __launch_bounds__(Tile<NARROW>::THREADS, 1)
     return true;
   };
   const int tiles = a.p_tiles * a.q_tiles, ncs_l = (a.steps_l + 1) / 2;
+  // this pair's part of K: the code stages c0 .. c1 - 1 of shards * ncs_l, at two steps each (a shard's last may have one)
+  const int c0 = int(int64_t(a.shards) * ncs_l * split / a.splits), c1 = int(int64_t(a.shards) * ncs_l * (split + 1) / a.splits);
+  const int r0 = c0 / ncs_l, r1 = (c1 - 1) / ncs_l;
+  const int first0 = 2 * (c0 % ncs_l), end1 = min(2 * ((c1 - 1) % ncs_l) + 2, a.steps_l);
+  auto first_step = [&](int r) { return r == r0 ? first0 : 0; };      // steps of shard r: from first_step to end_step - 1
+  auto end_step = [&](int r) { return r == r1 ? end1 : a.steps_l; };
   // first weight row (gate row) of a row tile; the stored rows of shard r of K begin at r * rows
   auto tile_row = [&](int p) -> int64_t {
     if (!SILU) return (int64_t(p) * 2 + rank) * kRows;
@@ -180,8 +191,8 @@ __global__ void __launch_bounds__(Tile<NARROW>::THREADS, 1)
     pdl_wait();   // the tokens may come from the kernel before; the weights are constants
     for (int tile = pair; tile < tiles && ok; tile += pairs) {
       const int m0 = tile / a.p_tiles * a.bn + rank * (a.bn / 2);
-      for (int r = 0; r < a.shards && ok; ++r)
-        for (int k = 0; k < a.steps_l; ++k, ++n) {
+      for (int r = r0; r <= r1 && ok; ++r)
+        for (int k = first_step(r); k < end_step(r); ++k, ++n) {
           const uint32_t s = n % XS, dst = sx + s * T::X_BYTES;
           ok = wait(T::B_X_EMPTY + s, ((n / XS) & 1) ^ 1, 2u);
           if (!ok) break;
@@ -199,8 +210,8 @@ __global__ void __launch_bounds__(Tile<NARROW>::THREADS, 1)
     bool ok = true;
     for (int tile = pair; tile < tiles && ok; tile += pairs) {
       const int row = int(tile_row(tile % a.p_tiles));
-      for (int r = 0; r < a.shards && ok; ++r)
-        for (int c = 0; c < ncs_l; ++c, ++n) {
+      for (int r = r0; r <= r1 && ok; ++r)
+        for (int c = first_step(r) / 2; 2 * c < end_step(r); ++c, ++n) {
           const uint32_t s = n % CS, dst = sc + s * T::C_BYTES;
           ok = wait(T::B_C_EMPTY + s, ((n / CS) & 1) ^ 1, 1u);
           if (!ok) break;
@@ -224,8 +235,8 @@ __global__ void __launch_bounds__(Tile<NARROW>::THREADS, 1)
         const uint32_t d = tmem + (u & 1) * T::TOKENS;
         uint32_t add = 0;
         ok = wait(T::B_ACC_EMPTY + (u & 1), ((u >> 1) & 1) ^ 1, 4u);
-        for (int r = 0; r < a.shards && ok; ++r)
-          for (int i = 0; i < a.steps_l; ++i, ++n) {
+        for (int r = r0; r <= r1 && ok; ++r)
+          for (int i = first_step(r); i < end_step(r); ++i, ++n) {
             const uint32_t s = n % XS, h = n % AS;
             ok = wait(T::B_X_FULL + s, (n / XS) & 1, 8u) && wait(T::B_A_FULL + h, (n / AS) & 1, 16u);
             if (!ok) break;
@@ -236,12 +247,12 @@ __global__ void __launch_bounds__(Tile<NARROW>::THREADS, 1)
               umma_ts(lead, d, at + k * 8, b + (k >> 2) * (T::X_HALF >> 4) + 2 * (k & 3), b_hi, idesc, add);
               add = 1;
             }
-            umma_commit_pair(lead, bar(T::B_A_EMPTY + h));
-            umma_commit_pair(lead, bar(T::B_X_EMPTY + s));
+            umma_commit_pair(lead, bar(T::B_A_EMPTY + h), both);
+            umma_commit_pair(lead, bar(T::B_X_EMPTY + s), both);
           }
-        if (ok) umma_commit_pair(lead, bar(T::B_ACC_FULL + (u & 1)));
+        if (ok) umma_commit_pair(lead, bar(T::B_ACC_FULL + (u & 1)), both);
       }
-      umma_commit_pair(lead, bar(T::B_DRAIN));
+      umma_commit_pair(lead, bar(T::B_DRAIN), both);
       tcx::mbar_wait(bar(T::B_DRAIN), 0, &g_w4_error, 32u);
     }
   } else if (warp >= 4 && warp < T::EPILOGUE0) {
@@ -252,20 +263,24 @@ __global__ void __launch_bounds__(Tile<NARROW>::THREADS, 1)
     const int64_t row_off = SILU ? (lane >> 4) * a.i_l + 16 * q + (lane & 15) : srow;
     const uint32_t code_row = sc + uint32_t(srow) * 128u, tmem_row = tmem + (uint32_t(32 * q) << 16) + T::A;
     const uint16_t* scales = reinterpret_cast<const uint16_t*>(a.w.scales);
-    // the step: number n, its tile, shard r of K, place k in the shard; cs0: code stages before this shard
-    int tile = pair, r = 0, k = set;
-    uint32_t n = set, cs0 = 0;
+    // the step: number n, its tile, shard r of K, place k in the shard, which ends at k_end; cs0: code stages before the
+    // shard's first (less those of the shard that are not this pair's)
+    int tile = pair, r = r0, k = first0 + set, k_end = end_step(r0);
+    uint32_t n = set, cs0 = uint32_t(-(first0 / 2));
     const uint16_t* sp = nullptr;   // scales and zeros of this thread's row in the step's shard
     const uint8_t* zp = nullptr;
     bool have = false;
     auto settle = [&]() {   // k may lie past its shard
-      while (k >= a.steps_l) {
-        k -= a.steps_l;
-        cs0 += ncs_l;
-        if (++r == a.shards) {
-          r = 0;
+      while (k >= k_end) {
+        cs0 += (k_end + 1) / 2;
+        k -= k_end;
+        if (++r > r1) {
+          r = r0;
           tile += pairs;
+          k += first0;
+          cs0 -= first0 / 2;
         }
+        k_end = end_step(r);
       }
       if (tile >= tiles) return;
       const int64_t row = tile_row(tile % a.p_tiles) + row_off, at = (int64_t(r) * a.rows + row) * a.w.groups;
@@ -290,13 +305,13 @@ __global__ void __launch_bounds__(Tile<NARROW>::THREADS, 1)
     while (tile < tiles) {
       const uint32_t cs = cs0 + uint32_t(k >> 1), st = cs % CS, in_stage = uint32_t(k & 1);
       const uint32_t h = n % AS, a_parity = ((n / AS) & 1) ^ 1;
-      const uint32_t arrivals = k == a.steps_l - 1 && !in_stage ? 2u : 1u;   // for the step that its code stage lacks, too
+      const uint32_t arrivals = k == k_end - 1 && !in_stage ? 2u : 1u;   // for the step that its code stage lacks, too
       uint32_t s2[NG], z2[NG];
 #pragma unroll
       for (int e = 0; e < NG; ++e) s2[e] = scale_pair(s[e]), z2[e] = offset_pair(z[e]);
       n += T::SETS;
       k += T::SETS;
-      if (k >= a.steps_l) settle();
+      if (k >= k_end) settle();
       if (tile < tiles) load_scales();   // of this warp's next step, in flight meanwhile
       if (!__all_sync(0xffffffffu, wait(T::B_C_FULL + st, (cs / CS) & 1, 64u))) break;   // the warp goes on as one
       uint4 v[4];
@@ -349,6 +364,16 @@ __global__ void __launch_bounds__(Tile<NARROW>::THREADS, 1)
         o = (int64_t(p) * 2 + rank) * kRows + 32 * q + lane;
         have = o < a.rows;
       }
+      if (a.splits > 1) {   // to the cluster: the sum of this part of K, [token][row] over the token stages, which are done
+        for (int c = 0; c < a.bn; c += 32) {
+          uint32_t v[32];
+          tmem_ld32_arrived(d + c, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(sx + uint32_t((c + i) * kRows + 32 * q + lane) * 4u), "r"(v[i]) : "memory");
+        }
+        break;
+      }
       const bool pairs_of = !SILU && even && (int64_t(p) * 2 + rank) * kRows + 32 * q + 32 <= a.rows;
       for (int c = 0; c < a.bn; c += 32) {
         uint32_t v[32];
@@ -396,6 +421,33 @@ __global__ void __launch_bounds__(Tile<NARROW>::THREADS, 1)
   __syncwarp();
   tcx::tc_fence_before();
   cluster_sync_all();   // neither CTA leaves while the other may arrive at its barriers or use its TMEM
+  if (a.splits > 1) {
+    // the parts' sums in their order; the pairs take the tokens in shares, two at a time
+    const int row = threadIdx.x & 127, q = row >> 5, tile = pair, p = tile % a.p_tiles, m0 = tile / a.p_tiles * a.bn;
+    const int64_t j = SILU ? (int64_t(p % a.shard_tiles) * 2 + rank) * (kRows / 2) + 16 * q + (lane & 15) : 0;
+    const int64_t o = SILU ? int64_t(p / a.shard_tiles) * a.i_l + j : (int64_t(p) * 2 + rank) * kRows + row;
+    const bool have = SILU ? j < a.i_l : o < a.rows;
+    const int end = a.bn / 2 * (split + 1) / a.splits;
+    for (int t = a.bn / 2 * split / a.splits + (threadIdx.x >> 7); t < end; t += T::THREADS / 128) {
+      float v0 = 0.0f, v1 = 0.0f;
+      for (int s = 0; s < a.splits; ++s) {
+        const uint32_t at = map_to_rank(sx + uint32_t(2 * t * kRows + row) * 4u, uint32_t(2 * s + rank));
+        v0 += ld_cluster_f32(at);
+        v1 += ld_cluster_f32(at + kRows * 4);
+      }
+      const int m = m0 + 2 * t;
+      if (SILU) {
+        const float got = __shfl_xor_sync(0xffffffffu, lane < 16 ? v1 : v0, 16);
+        const float gate = lane < 16 ? v0 : got, up = lane < 16 ? got : v1;
+        const int mine = m + (lane >> 4);
+        if (have && mine < a.M) a.out[int64_t(mine) * a.ldc + o] = __float2bfloat16_rn(__fdividef(gate, 1.0f + __expf(-gate)) * up);
+      } else if (have) {
+        if (m < a.M) a.out[int64_t(m) * a.ldc + o] = __float2bfloat16_rn(v0);
+        if (m + 1 < a.M) a.out[int64_t(m + 1) * a.ldc + o] = __float2bfloat16_rn(v1);
+      }
+    }
+    cluster_sync_all();   // the others have read this CTA's sums
+  }
   if (warp == 1) {
     tcx::tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
@@ -410,13 +462,13 @@ static int launch(const CUtensorMap& mx, const CUtensorMap& mc, const TcArgs& a,
   if (set != cudaSuccess) return set_error(QW_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(set));
   const int tiles = a.p_tiles * a.q_tiles;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(2 * std::min(tiles, 76)));
+  cfg.gridDim = dim3(unsigned(a.splits > 1 ? 2 * a.splits * tiles : 2 * std::min(tiles, kPairs)));
   cfg.blockDim = dim3(Tile<NARROW>::THREADS);
   cfg.dynamicSmemBytes = Tile<NARROW>::SMEM;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = unsigned(2 * a.splits);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -426,6 +478,21 @@ static int launch(const CUtensorMap& mx, const CUtensorMap& mc, const TcArgs& a,
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mx, mc, a);
   if (e != cudaSuccess) return set_error(QW_ERR_CUDA, "w4 gemm_tc_kernel launch: %s", cudaGetErrorString(e));
   return check_launch("w4 gemm_tc_kernel");
+}
+
+// Few tiles: their K in parts, as many as run at once (15 clusters of 8 CTAs, 23 of 6, 36 of 4, 76 pairs).  16 tokens,
+// K 8192, us in 4 / 3 / 2 / 1 parts: 15 tiles 13.4 / 15.2 / 18.5 / 28.6, 16 tiles 23.6 / 14.9 / 18.2 / 28.3,
+// 22 tiles 24.2 / 15.4 / 18.5 / 28.5, 36 tiles 35.6 / 28.8 / 19.0 / 28.9.
+static int parts_of_k(int64_t tiles, int64_t stages) {
+  return int(std::min<int64_t>(tiles <= 15 ? 4 : tiles <= 23 ? 3 : tiles <= 36 ? 2 : 1, stages));
+}
+static int64_t row_tiles(int64_t N, int silu_shards) {   // silu_shards: shards of a SiluAndMul, else 0
+  return silu_shards ? silu_shards * ((N / 2 / silu_shards + kRows - 1) / kRows) : (N + 2 * kRows - 1) / (2 * kRows);
+}
+// steps of 128 columns that the busiest pair walks through with one tile of tokens
+int64_t tc_steps(int64_t N, int64_t K_l, int silu_shards, int shards) {
+  const int64_t tiles = row_tiles(N, silu_shards), stages = shards * ((K_l + 255) / 256), parts = parts_of_k(tiles, stages);
+  return (tiles * parts + kPairs - 1) / kPairs * 2 * ((stages + parts - 1) / parts);
 }
 
 int gemm_tc(const bf16* x, const Weights& w, bf16* out, int64_t M, int64_t N, int64_t K, int shards, int tp, bool silu,
@@ -442,11 +509,12 @@ int gemm_tc(const bf16* x, const Weights& w, bf16* out, int64_t M, int64_t N, in
   a.bn = int((M + a.q_tiles - 1) / a.q_tiles + 15) / 16 * 16;
   a.q_tiles = int((M + a.bn - 1) / a.bn);
   a.shard_tiles = silu ? int((a.i_l + kRows - 1) / kRows) : 0;
-  const int64_t p_tiles = silu ? int64_t(tp) * a.shard_tiles : (N + 2 * kRows - 1) / (2 * kRows);
-  if (p_tiles * a.q_tiles >= (int64_t(1) << 31)) return set_error(QW_ERR_SHAPE, "qw_w4_gemm: too many output tiles");
+  const int64_t p_tiles = row_tiles(N, silu ? tp : 0);
+  if (p_tiles * a.q_tiles >= (int64_t(1) << 30)) return set_error(QW_ERR_SHAPE, "qw_w4_gemm: too many output tiles");
   a.p_tiles = int(p_tiles);
   a.shards = shards;
   a.steps_l = int((K_l + 127) / 128);
+  a.splits = parts_of_k(p_tiles * a.q_tiles, int64_t(shards) * ((a.steps_l + 1) / 2));
   CUtensorMap mx, mc;
   const uint64_t xd[3] = {uint64_t(K_l), uint64_t(shards), uint64_t(M)}, xst[2] = {uint64_t(K_l) * 2, uint64_t(K) * 2};
   const uint32_t xb[3] = {64, 1, uint32_t(a.bn / 2)};

@@ -13,6 +13,7 @@ int check_weights(const char* who, const void* codes, const void* scales, int64_
 Weights make_weights(const void* codes, const void* scales, const void* zeros, int64_t K, int group);
 int gemm_tc(const bf16* x, const Weights& w, bf16* out, int64_t M, int64_t N, int64_t K, int shards, int tp, bool silu,
             cudaStream_t st);
+int64_t tc_steps(int64_t N, int64_t K_l, int silu_shards, int shards);
 
 struct GemvArgs {
   const bf16* x;         // [M, K]
@@ -27,13 +28,6 @@ struct GemvArgs {
   int split;             // warps that share a row tile, each every split-th chunk of 128 columns
 };
 
-__device__ __forceinline__ uint4 ldg_codes(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -44,17 +38,26 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
 }
 
 constexpr int kWarps = 8;
-constexpr size_t gemv_smem(int nt, int r) { return size_t(kWarps) * 16 * r * (nt * 8 + 1) * 4; }
+// a warp's shared memory: DEPTH chunks of codes, in whose place its sums come at the end
+constexpr size_t gemv_warp_smem(int nt, int r, int depth) {
+  const size_t codes = size_t(depth) * r * 1024, sums = size_t(16) * r * (nt * 8 + 1) * 4;
+  return ((codes > sums ? codes : sums) + 15) / 16 * 16;
+}
 
 // A warp takes R tiles of 16 weight rows and every split-th chunk of 128 columns; lane (g, t) = (lane / 4,
 // lane % 4) holds the 32 columns of piece t of rows g and g + 8.  The k index of an MMA may be any
 // permutation that weights and tokens share, so a lane's own columns are its k values: no shuffles.
-// The codes of PF chunks are in flight at once, the first ones ahead of the programmatic wait.
+// The codes of DEPTH chunks are in flight at once, the first ones ahead of the programmatic wait: each lane copies
+// asynchronously to shared memory what it reads there itself, so that the depth costs no registers and nothing waits
+// for another lane.
 // WHOLE: a shard's columns are whole chunks, so that nothing in the loop has a condition of its own lane.
-template <int NT, int R, int PF, bool SILU, bool ZEROS, bool WHOLE>
+template <int NT, int R, int DEPTH, bool SILU, bool ZEROS, bool WHOLE>
 __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(GemvArgs a) {
-  extern __shared__ float red_dyn[];   // [kWarps][16 R][NT * 8 + 1]
-  float(*red)[16 * R][NT * 8 + 1] = reinterpret_cast<float(*)[16 * R][NT * 8 + 1]>(red_dyn);
+  extern __shared__ __align__(16) uint8_t gemv_dyn[];
+  constexpr size_t WARP_SMEM = gemv_warp_smem(NT, R, DEPTH);
+  auto sum_at = [&](int w, int row, int n) -> float& {
+    return reinterpret_cast<float*>(gemv_dyn + w * WARP_SMEM)[row * (NT * 8 + 1) + n];
+  };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int per_cta = kWarps / a.split, sl = warp % a.split;
   const int64_t tile0 = int64_t(blockIdx.x) * per_cta * R, tile = tile0 + warp / a.split * R;
@@ -88,12 +91,12 @@ __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(GemvArgs a) {
     }
   }
   const int64_t to_shard_c = (a.rows - 1) * a.w.row_bytes, to_shard_s = (a.rows - 1) * a.w.groups;
-  struct Chunk {
-    uint4 c[R][2];
+  const uint32_t ring = smem_u32(gemv_dyn + warp * WARP_SMEM) + uint32_t(lane) * 16u;
+  struct Scales {
     uint32_t s[R][2], z[R][2];
   };
-  Chunk buf[PF];
-  auto load = [&](Chunk& b) {
+  // codes of the next chunk to ring slot d, its scales to b
+  auto load = [&](int d, Scales& b) {
     while (lu >= a.pieces_l && left > 0) {   // on to the next shard's rows
       lu -= a.pieces_l;
 #pragma unroll
@@ -112,12 +115,11 @@ __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(GemvArgs a) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (!WHOLE) {
-          b.c[q][e] = make_uint4(0, 0, 0, 0);
           b.s[q][e] = 0;
           b.z[q][e] = 8;
         }
         if (left > 0) {
-          b.c[q][e] = ldg_codes(cp[q][e]);
+          cp_async16(ring + uint32_t((d * R + q) * 2 + e) * 512u, cp[q][e]);
           b.s[q][e] = __ldg(sp[q][e]);
           if (ZEROS) b.z[q][e] = __ldg(zp[q][e]);
         }
@@ -125,6 +127,7 @@ __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(GemvArgs a) {
         sp[q][e] += step;
         if (ZEROS) zp[q][e] += step;
       }
+    cp_async_commit();
     lu += advance;
     left -= advance;
   };
@@ -133,8 +136,9 @@ __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(GemvArgs a) {
   for (int q = 0; q < R; ++q)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[q][n][0] = acc[q][n][1] = acc[q][n][2] = acc[q][n][3] = 0.0f;
+  Scales sc[DEPTH];
 #pragma unroll
-  for (int d = 0; d < PF; ++d) load(buf[d]);
+  for (int d = 0; d < DEPTH; ++d) load(d, sc[d]);
   pdl_wait();
   pdl_trigger();
   // this lane's token of each group of 8; past the last one it is token 0, whose sums there are not stored
@@ -144,9 +148,9 @@ __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(GemvArgs a) {
     const int tok = m0 + n * 8 + g;
     xp[n] = a.x + int64_t(tok < a.M ? tok : 0) * a.K + (4 * sl + t) * kPiece;
   }
-  for (int u0 = 4 * sl; u0 < a.pieces; u0 += advance * PF) {
+  for (int u0 = 4 * sl; u0 < a.pieces; u0 += advance * DEPTH) {
 #pragma unroll
-    for (int d = 0; d < PF; ++d) {
+    for (int d = 0; d < DEPTH; ++d) {
       const int u = u0 + advance * d;
       if (u >= a.pieces) break;
       const bool in = WHOLE || u + t < a.pieces;
@@ -161,7 +165,19 @@ __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(GemvArgs a) {
       constexpr int AHEAD = NT <= 2 ? 4 : NT <= 6 ? 2 : 1;   // words of tokens in flight
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) load_x(i);
-      Chunk& b = buf[d];
+      cp_async_wait<DEPTH - 1>();
+      uint4 c[R][2];
+#pragma unroll
+      for (int q = 0; q < R; ++q)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(c[q][e].x), "=r"(c[q][e].y), "=r"(c[q][e].z), "=r"(c[q][e].w)
+                       : "r"(ring + uint32_t((d * R + q) * 2 + e) * 512u)
+                       : "memory");
+          if (!WHOLE && !in) c[q][e] = make_uint4(0, 0, 0, 0);   // nothing was copied there
+        }
+      const Scales& b = sc[d];
       uint32_t s2[R][2], z2[R][2];
 #pragma unroll
       for (int q = 0; q < R; ++q)
@@ -172,8 +188,8 @@ __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(GemvArgs a) {
 #pragma unroll
         for (int q = 0; q < R; ++q) {
           uint32_t pa[4], pb[4];
-          const uint32_t wa = i == 0 ? b.c[q][0].x : i == 1 ? b.c[q][0].y : i == 2 ? b.c[q][0].z : b.c[q][0].w;
-          const uint32_t wb = i == 0 ? b.c[q][1].x : i == 1 ? b.c[q][1].y : i == 2 ? b.c[q][1].z : b.c[q][1].w;
+          const uint32_t wa = i == 0 ? c[q][0].x : i == 1 ? c[q][0].y : i == 2 ? c[q][0].z : c[q][0].w;
+          const uint32_t wb = i == 0 ? c[q][1].x : i == 1 ? c[q][1].y : i == 2 ? c[q][1].z : c[q][1].w;
           decode(wa, magic, z2[q][0], s2[q][0], pa);
           decode(wb, magic, z2[q][1], s2[q][1], pb);
 #pragma unroll
@@ -186,17 +202,19 @@ __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(GemvArgs a) {
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) xp[n] += advance * kPiece;
-      load(b);
+      load(d, sc[d]);
     }
   }
+  cp_async_wait<0>();   // nothing is on its way into the places of the sums
+  __syncwarp();
 #pragma unroll
   for (int q = 0; q < R; ++q)
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      red[warp][16 * q + g][n * 8 + 2 * t] = acc[q][n][0];
-      red[warp][16 * q + g][n * 8 + 2 * t + 1] = acc[q][n][1];
-      red[warp][16 * q + g + 8][n * 8 + 2 * t] = acc[q][n][2];
-      red[warp][16 * q + g + 8][n * 8 + 2 * t + 1] = acc[q][n][3];
+      sum_at(warp, 16 * q + g, n * 8 + 2 * t) = acc[q][n][0];
+      sum_at(warp, 16 * q + g, n * 8 + 2 * t + 1) = acc[q][n][1];
+      sum_at(warp, 16 * q + g + 8, n * 8 + 2 * t) = acc[q][n][2];
+      sum_at(warp, 16 * q + g + 8, n * 8 + 2 * t + 1) = acc[q][n][3];
     }
   __syncthreads();
   constexpr int out_rows = SILU ? 8 : 16;   // of a tile
@@ -208,37 +226,54 @@ __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(GemvArgs a) {
     float v = 0.0f, up = 0.0f;
     for (int s = 0; s < a.split; ++s) {   // in slice order
       const int w = lt / R * a.split + s, row = lt % R * 16 + r;
-      v += red[w][row][n];
-      if (SILU) up += red[w][row + 8][n];
+      v += sum_at(w, row, n);
+      if (SILU) up += sum_at(w, row + 8, n);
     }
     if (SILU) v = __fdividef(v, 1.0f + __expf(-v)) * up;
     a.out[int64_t(m0 + n) * a.ldc + o] = __float2bfloat16_rn(v);
   }
 }
 
-template <int NT, int R, int PF, bool SILU, bool ZEROS, bool WHOLE>
+// warps that share a unit of row tiles: up to 8, while there are no more than 32 such warps an SM
+static int gemv_split(int64_t units, int chunks) {
+  int split = kWarps;
+  while (split > 1 && (split > chunks || units * split > 152 * 32)) split >>= 1;
+  return split;
+}
+
+// 9 to 64 tokens: whether the tcgen05 kernel is expected to be done first.  Both sides from measurements: a step of
+// 256 rows x 128 columns takes a pair of SMs 0.39 us, the launch and its ends about 5; here 2.5 us and 0.21, 0.39, 0.46,
+// 0.46, 0.6 and 0.78 us for each 2^20 weights with 2, 3, 4, 5, 6 and 8 groups of 8 tokens.  us there and here:
+// 8192 x 8192, 16 tokens 19.0 / 15.7, 24 19.3 / 20.8, 64 20.4 / 50.2; 4096 x 4096, 24 11.3 / 8.7, 64 12.2 / 15.6;
+// 4096 x 1024, 64 8.4 / 7.2; 151936 x 1024, 16 31.2 / 36.5, 64 32.7 / 145.
+static bool tc_is_faster(int nt, int64_t N, int64_t K, int64_t K_l, int silu_shards, int shards) {
+  static const double per_mega[9] = {0, 0, 0.21, 0.39, 0.46, 0.46, 0.6, 0.78, 0.78};
+  const double here = 2.5 + per_mega[nt] * double(N) * double(K) / (1 << 20);
+  return 5.0 + 0.39 * double(tc_steps(N, K_l, silu_shards, shards)) < here;
+}
+
+template <int NT, int R, int DEPTH, bool SILU, bool ZEROS, bool WHOLE>
 static int launch_gemv(GemvArgs a, cudaStream_t st) {
-  auto kern = gemv_kernel<NT, R, PF, SILU, ZEROS, WHOLE>;
-  constexpr size_t smem = gemv_smem(NT, R);
+  auto kern = gemv_kernel<NT, R, DEPTH, SILU, ZEROS, WHOLE>;
+  constexpr size_t smem = kWarps * gemv_warp_smem(NT, R, DEPTH);
   if (smem > 48 * 1024) {
     static const cudaError_t set = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (set != cudaSuccess) return set_error(QW_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(set));
   }
   const int chunks = (a.pieces + 3) / 4;
   const int64_t units = (a.tiles + R - 1) / R;
-  a.split = 8;
-  while (a.split > 1 && (a.split > chunks || units * a.split > 152 * 32)) a.split >>= 1;
+  a.split = gemv_split(units, chunks);
   const int per_cta = kWarps / a.split;
   const dim3 grid(unsigned((units + per_cta - 1) / per_cta), unsigned((a.M + NT * 8 - 1) / (NT * 8)));
   launch_pdl(kern, grid, kWarps * 32, smem, st, a);
   return check_launch("w4 gemv");
 }
 
-template <int NT, int R, int PF, bool WHOLE>
+template <int NT, int R, int DEPTH, bool WHOLE>
 static int launch_gemv(const GemvArgs& a, bool silu, cudaStream_t st) {
   if (a.w.zeros != nullptr)
-    return silu ? launch_gemv<NT, R, PF, true, true, WHOLE>(a, st) : launch_gemv<NT, R, PF, false, true, WHOLE>(a, st);
-  return silu ? launch_gemv<NT, R, PF, true, false, WHOLE>(a, st) : launch_gemv<NT, R, PF, false, false, WHOLE>(a, st);
+    return silu ? launch_gemv<NT, R, DEPTH, true, true, WHOLE>(a, st) : launch_gemv<NT, R, DEPTH, false, true, WHOLE>(a, st);
+  return silu ? launch_gemv<NT, R, DEPTH, true, false, WHOLE>(a, st) : launch_gemv<NT, R, DEPTH, false, false, WHOLE>(a, st);
 }
 
 static int linear(const bf16* x, const void* codes, const void* scales, const void* zeros, bf16* out, int64_t M, int64_t N,
@@ -257,17 +292,25 @@ static int linear(const bf16* x, const void* codes, const void* scales, const vo
   a.K = int(K);
   a.pieces = int(K / kPiece);
   a.pieces_l = int(K_l / kPiece);
-  if (M > 64) return gemm_tc(x, a.w, out, M, N, K, mode == QW_GEMM_ROW_REDUCE ? tp : 1, tp, silu, st);
-  const int nt = int((M + 7) / 8);
-  if (a.pieces_l % 4) return nt <= 1 ? launch_gemv<1, 1, 2, false>(a, silu, st) : launch_gemv<4, 1, 1, false>(a, silu, st);
+  const int shards = mode == QW_GEMM_ROW_REDUCE ? tp : 1, nt = int((M + 7) / 8);
+  const bool whole = a.pieces_l % 4 == 0;
+  if (nt > 8 || (nt > 1 && tc_is_faster(nt, N, K, K_l, silu ? tp : 0, shards)) || (nt > 1 && !whole))
+    return gemm_tc(x, a.w, out, M, N, K, shards, tp, silu, st);
+  if (!whole) return launch_gemv<1, 1, 2, false>(a, silu, st);
   switch (nt) {
-    case 1: return launch_gemv<1, 1, 2, true>(a, silu, st);
+    case 1: {
+      // Two row tiles a warp halve the tokens' traffic through L1 (8 x 16 lines a load), one tile leaves more warps:
+      // 4 x 8192 x 8192 18.4 us with one, 11.1 with two, 8 x 151936 x 1024 30.0 and 25.6; 8 x 12288 x 2048, where a
+      // warp has two chunks, 7.3 and 8.7; 1 x 28672 x 8192 29.5 and 36.5.
+      const int chunks = a.pieces / 4, split = gemv_split(a.tiles, chunks);
+      return M > 2 && chunks >= 4 * split ? launch_gemv<1, 2, 2, true>(a, silu, st) : launch_gemv<1, 1, 4, true>(a, silu, st);
+    }
     case 2: return launch_gemv<2, 2, 2, true>(a, silu, st);
     case 3: return launch_gemv<3, 2, 2, true>(a, silu, st);
     case 4: return launch_gemv<4, 2, 2, true>(a, silu, st);
     case 5: return launch_gemv<5, 2, 2, true>(a, silu, st);
     case 6: return launch_gemv<6, 2, 2, true>(a, silu, st);
-    default: return launch_gemv<8, 2, 1, true>(a, silu, st);
+    default: return launch_gemv<8, 2, 2, true>(a, silu, st);
   }
 }
 

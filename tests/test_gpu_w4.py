@@ -212,6 +212,9 @@ SHAPES = [
     # more tiles than pairs of SMs, and K (or its shards) that ends inside 128 columns, or is shorter
     (1999, 3001, 320, 64, 1, COL, NONE), (1500, 2500, 320, 32, 10, ROW, NONE), (1500, 2500, 576, 64, 3, ROW, NONE),
     (2100, 4096, 448, 64, 2, COL, SILU), (1200, 4000, 32, 32, 1, COL, NONE),
+    # few tiles over a long K, whose parts end inside and between shards
+    (70, 500, 3200, 64, 5, ROW, NONE), (90, 1000, 4096, 128, 1, COL, NONE), (128, 4600, 1664, 128, 1, COL, NONE),
+    (190, 256, 5760, 32, 9, ROW, NONE), (100, 2240, 2080, 32, 5, COL, SILU), (180, 7000, 1408, 128, 1, COL, NONE),
 ]
 
 
