@@ -6,6 +6,8 @@ namespace qw {
 template <typename T>
 int launch_gather_rows(const void* src, int64_t n_src, const int32_t* idx, int64_t n, int64_t H, void* out,
                        cudaStream_t st);
+template <typename T>
+int launch_argmax(const void* logits, int64_t M, int64_t V, int64_t* out, cudaStream_t st);
 
 namespace w4 {
 
@@ -414,6 +416,7 @@ extern "C" int qw_w4_lm_head(const void* hidden, int64_t T, const int32_t* last_
   int e = w4::linear(static_cast<const bf16*>(x), codes, scales, zeros, static_cast<bf16*>(logits), n_out, V, H, group, 1,
                      QW_GEMM_COLUMN, QW_EPI_NONE, st);
   if (e || !next_tokens) return e;
+  if (V % 8 == 0) return launch_argmax<bf16>(logits, n_out, V, next_tokens, st);   // whole 16-byte pieces
   launch_pdl(w4::argmax_kernel, unsigned(n_out), 1024, 0, st, static_cast<const bf16*>(logits), V, next_tokens);
   return check_launch("qw_w4_lm_head");
 }

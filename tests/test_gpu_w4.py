@@ -126,6 +126,33 @@ def test_quantize(L, N, K, group, zeros):
     assert torch.equal(codes.cpu(), put(n))
 
 
+@pytest.mark.parametrize("zeros", [False, True])
+def test_quantize_every_quotient(L, zeros):
+    """Every pair of 8-bit significands: w = a * 2^i against the scale that a group's largest weight b gives it,
+    ties among them.  A group holds one b (its negative too, asymmetric) and 31 of the a."""
+    a = torch.arange(128, 256).double()
+    w = []
+    for i in range(-5, 1):
+        x = (a * 2.0 ** i)[None, :].expand(128, 128)
+        b = (a * 2.0)[:, None]                                     # the largest of its group
+        x = torch.minimum(x, b)
+        for part in (x[:, 0:30], x[:, 30:60], x[:, 60:90], x[:, 90:120], x[:, 98:128]):
+            sign = torch.where(torch.arange(30) % 2 == 0, 1.0, -1.0) if i % 2 else torch.ones(30)
+            for low in ((0.0, 0.25, 1.0) if zeros else (0.0,)):
+                w.append(torch.cat([b, -low * b, part * sign], 1))
+    w = torch.cat(w).bfloat16()
+    n, s, z = quantize_ref(w, 32, zeros)
+    N = w.shape[0]
+    codes = torch.empty(N, 16, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(N, 1, dtype=torch.bfloat16, device="cuda")
+    zs = torch.empty(N, 1, dtype=torch.uint8, device="cuda") if zeros else None
+    L.w4_quantize(w.cuda(), 32, codes, scales, zs)
+    sync_ok(L)
+    assert torch.equal(scales.cpu(), s) and torch.equal(codes.cpu(), put(n))
+    if zeros:
+        assert torch.equal(zs.cpu(), z)
+
+
 def test_quantize_error_is_half_a_step(L):
     """Each weight within half a scale, and the clamp of the rounded scale, of what it was."""
     w = torch.randn(64, 1024, generator=gen(2)).bfloat16()
