@@ -637,14 +637,17 @@ int qw_w4_embed_vocab(const int64_t* ids, int64_t T, const void* codes, const vo
  *     C [M, N/2] = silu(gate) * up is formed from the fp32 sums.
  *   QW_GEMM_ROW_REDUCE: codes [tp, N, K/tp/2], scales and zeros
  *     [tp, N, K/tp/group]; any N.
- * Any M below 2^21.  A and C 16-byte aligned.  The weights may be read before
- * the kernels enqueued earlier on the stream have ended, unless one of those
- * is qw_w4_quantize or a kernel outside this library.
+ * Any M below 2^21.  A and C 16-byte aligned.
+ * flags: 0, or QW_W4_WEIGHTS_READY: the caller states that codes, scales and
+ *   zeros were complete before the kernel enqueued just before this call
+ *   started (weights that were loaded once).  They are then read before that
+ *   kernel has ended (programmatic dependent launch); without the flag nothing is.
  * workspace: qw_w4_gemm_workspace_size bytes; may be NULL when that is 0.
  */
+#define QW_W4_WEIGHTS_READY 1
 int qw_w4_gemm(const void* A, const void* codes, const void* scales, const void* zeros, void* C, int64_t M, int64_t N,
                int64_t K, int group, int tp, int mode, int epilogue, void* workspace, size_t workspace_bytes, int dtype,
-               void* stream);
+               int flags, void* stream);
 size_t qw_w4_gemm_workspace_size(int64_t M, int64_t N, int64_t K, int tp, int mode, int epilogue);
 
 /*
@@ -653,11 +656,11 @@ size_t qw_w4_gemm_workspace_size(int64_t M, int64_t N, int64_t K, int tp, int mo
  * zero row), and with next_tokens the argmax over each row of the rounded
  * logits, lowest index on ties.  V any number that tp divides.
  * workspace: qw_w4_lm_head_workspace_size bytes, 16-byte aligned; may be NULL
- * when last_idx and next_tokens both are.
+ * when last_idx and next_tokens both are.  flags: as for qw_w4_gemm.
  */
 int qw_w4_lm_head(const void* hidden, int64_t T, const int32_t* last_idx, int64_t n_out, const void* codes,
                   const void* scales, const void* zeros, int64_t V, int64_t H, int group, int tp, void* logits,
-                  int64_t* next_tokens, void* workspace, size_t workspace_bytes, int dtype, void* stream);
+                  int64_t* next_tokens, void* workspace, size_t workspace_bytes, int dtype, int flags, void* stream);
 size_t qw_w4_lm_head_workspace_size(int64_t n_out, int64_t V, int64_t H, int tp);
 
 /*

@@ -69,9 +69,9 @@ SIGNATURES = {
     "qw_sample_workspace_size": (C.c_size_t, [_i64, _i64]),
     "qw_w4_quantize": (C.c_int, [_p, _i64, _i64, _i32, _p, _p, _p, _i32, _p]),
     "qw_w4_embed_vocab": (C.c_int, [_p, _i64, _p, _p, _p, _i64, _i64, _i32, _i32, _p, _p, _i32, _p]),
-    "qw_w4_gemm": (C.c_int, [_p, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _i32, _i32, _i32, _p, _sz, _i32, _p]),
+    "qw_w4_gemm": (C.c_int, [_p, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _i32, _i32, _i32, _p, _sz, _i32, _i32, _p]),
     "qw_w4_gemm_workspace_size": (C.c_size_t, [_i64, _i64, _i64, _i32, _i32, _i32]),
-    "qw_w4_lm_head": (C.c_int, [_p, _i64, _p, _i64, _p, _p, _p, _i64, _i64, _i32, _i32, _p, _p, _p, _sz, _i32, _p]),
+    "qw_w4_lm_head": (C.c_int, [_p, _i64, _p, _i64, _p, _p, _p, _i64, _i64, _i32, _i32, _p, _p, _p, _sz, _i32, _i32, _p]),
     "qw_w4_lm_head_workspace_size": (C.c_size_t, [_i64, _i64, _i64, _i32]),
     "qw_selftest_wait_timeout": (C.c_int, [_p]),
     "qw_add_rmsnorm_gemm": (C.c_int, [_p, _p, _p, _p, _f32, _p, _p, _i64, _i64, _i64, _i32, _i32, _i32, _p]),
@@ -526,9 +526,15 @@ def w4_gemm_workspace_size(M, N, K, tp, mode, epilogue) -> int:
     return load().qw_w4_gemm_workspace_size(M, N, K, tp, mode, epilogue)
 
 
+QW_W4_WEIGHTS_READY = 1
+
+
 def w4_gemm(A, codes, scales, zeros, C_out, N, group, tp=1, mode=QW_GEMM_COLUMN, epilogue=QW_EPI_NONE, workspace=None,
-            stream=None):
-    """gemm() with 4-bit weights; N: output features before SiluAndMul."""
+            stream=None, weights_ready=False):
+    """gemm() with 4-bit weights; N: output features before SiluAndMul.
+
+    weights_ready: the previous kernel on the stream, and those that may still run beside it, write none of the weights
+    (see QW_W4_WEIGHTS_READY in qw.h)."""
     M, K = A.shape
     shards = tp if mode == QW_GEMM_ROW_REDUCE else 1
     if tp > 0:
@@ -540,7 +546,7 @@ def w4_gemm(A, codes, scales, zeros, C_out, N, group, tp=1, mode=QW_GEMM_COLUMN,
     _check(load().qw_w4_gemm(
         _dev_ptr(A, "A"), _dev_ptr(codes, "codes"), _dev_ptr(scales, "scales"), _dev_ptr(zeros, "zeros"),
         _dev_ptr(C_out, "C"), M, N, K, group, tp, mode, epilogue, _dev_ptr(workspace, "workspace"), _w4_bytes(workspace),
-        dtype_code(A.dtype), _stream(stream)))
+        dtype_code(A.dtype), QW_W4_WEIGHTS_READY if weights_ready else 0, _stream(stream)))
 
 
 def w4_lm_head_workspace_size(n_out, V, H, tp) -> int:
@@ -548,7 +554,7 @@ def w4_lm_head_workspace_size(n_out, V, H, tp) -> int:
 
 
 def w4_lm_head(hidden, last_idx, n_out, codes, scales, zeros, group, tp, logits, next_tokens=None, workspace=None,
-               stream=None):
+               stream=None, weights_ready=False):
     """lm_head() over a 4-bit table [V, H]: logits of rows last_idx of hidden, and greedy tokens."""
     T, H = hidden.shape
     V = codes.shape[0]
@@ -563,7 +569,7 @@ def w4_lm_head(hidden, last_idx, n_out, codes, scales, zeros, group, tp, logits,
         _dev_ptr(hidden, "hidden"), T, _dev_ptr(last_idx, "last_idx"), n_out, _dev_ptr(codes, "codes"),
         _dev_ptr(scales, "scales"), _dev_ptr(zeros, "zeros"), V, H, group, tp, _dev_ptr(logits, "logits"),
         _dev_ptr(next_tokens, "next_tokens"), _dev_ptr(workspace, "workspace"), _w4_bytes(workspace),
-        dtype_code(hidden.dtype), _stream(stream)))
+        dtype_code(hidden.dtype), QW_W4_WEIGHTS_READY if weights_ready else 0, _stream(stream)))
 
 
 def sample_workspace_size(B, V) -> int:

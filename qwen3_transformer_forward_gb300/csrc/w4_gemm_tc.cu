@@ -47,6 +47,7 @@ struct TcArgs {
   int p_tiles, q_tiles;   // weight row tiles, token tiles
   int shard_tiles;        // SiluAndMul: row tiles of a shard
   int shards, steps_l;    // shards of K, steps of 128 columns of a shard (the last may end in zeros)
+  int early;              // the weights may be read ahead of the programmatic wait
   int splits;             // pairs that share a tile's K (a cluster, one tile each); 1: every pair walks over tiles
 };
 
@@ -183,12 +184,13 @@ __global__ void __launch_bounds__(Tile<NARROW>::THREADS, 1)
     return int64_t(r) * 2 * a.i_l + (int64_t(p % a.shard_tiles) * 2 + rank) * (kRows / 2);
   };
 
+  if (!a.early) pdl_wait();   // weights that the kernel before may have written
   if (warp == 0) {
     // ---- tokens: this CTA's half of each block ----
     const uint32_t lead = elect_one();
     uint32_t n = 0;
     bool ok = true;
-    pdl_wait();   // the tokens may come from the kernel before; the weights are constants
+    pdl_wait();   // the tokens may come from the kernel before
     for (int tile = pair; tile < tiles && ok; tile += pairs) {
       const int m0 = tile / a.p_tiles * a.bn + rank * (a.bn / 2);
       for (int r = r0; r <= r1 && ok; ++r)
@@ -496,7 +498,7 @@ int64_t tc_steps(int64_t N, int64_t K_l, int silu_shards, int shards) {
 }
 
 int gemm_tc(const bf16* x, const Weights& w, bf16* out, int64_t M, int64_t N, int64_t K, int shards, int tp, bool silu,
-            cudaStream_t st) {
+            int early, cudaStream_t st) {
   const int64_t K_l = K / shards;
   TcArgs a{};
   a.out = out;
@@ -505,6 +507,7 @@ int gemm_tc(const bf16* x, const Weights& w, bf16* out, int64_t M, int64_t N, in
   a.ldc = silu ? N / 2 : N;
   a.i_l = silu ? N / 2 / tp : 0;
   a.M = int(M);
+  a.early = early;
   a.q_tiles = int((M + Tile<false>::TOKENS - 1) / Tile<false>::TOKENS);
   a.bn = int((M + a.q_tiles - 1) / a.q_tiles + 15) / 16 * 16;
   a.q_tiles = int((M + a.bn - 1) / a.bn);

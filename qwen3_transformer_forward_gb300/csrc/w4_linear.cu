@@ -14,7 +14,7 @@ namespace w4 {
 int check_weights(const char* who, const void* codes, const void* scales, int64_t N, int64_t K, int group);
 Weights make_weights(const void* codes, const void* scales, const void* zeros, int64_t K, int group);
 int gemm_tc(const bf16* x, const Weights& w, bf16* out, int64_t M, int64_t N, int64_t K, int shards, int tp, bool silu,
-            cudaStream_t st);
+            int early, cudaStream_t st);
 int64_t tc_steps(int64_t N, int64_t K_l, int silu_shards, int shards);
 
 struct GemvArgs {
@@ -27,6 +27,7 @@ struct GemvArgs {
   int64_t tiles;         // row tiles of 16 (SiluAndMul: 8 gate and their 8 up rows)
   int M, K;
   int pieces, pieces_l;  // pieces of K, of a shard's K
+  int early;             // the weights may be read ahead of the programmatic wait
   int split;             // warps that share a row tile, each every split-th chunk of 128 columns
 };
 
@@ -49,7 +50,7 @@ constexpr size_t gemv_warp_smem(int nt, int r, int depth) {
 // A warp takes R tiles of 16 weight rows and every split-th chunk of 128 columns; lane (g, t) = (lane / 4,
 // lane % 4) holds the 32 columns of piece t of rows g and g + 8.  The k index of an MMA may be any
 // permutation that weights and tokens share, so a lane's own columns are its k values: no shuffles.
-// The codes of DEPTH chunks are in flight at once, the first ones ahead of the programmatic wait: each lane copies
+// The codes of DEPTH chunks are in flight at once, the first ones ahead of the programmatic wait (QW_W4_WEIGHTS_READY): each lane copies
 // asynchronously to shared memory what it reads there itself, so that the depth costs no registers and nothing waits
 // for another lane.
 // WHOLE: a shard's columns are whole chunks, so that nothing in the loop has a condition of its own lane.
@@ -138,10 +139,11 @@ __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(GemvArgs a) {
   for (int q = 0; q < R; ++q)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[q][n][0] = acc[q][n][1] = acc[q][n][2] = acc[q][n][3] = 0.0f;
+  if (!a.early) pdl_wait();
   Scales sc[DEPTH];
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) load(d, sc[d]);
-  pdl_wait();
+  if (a.early) pdl_wait();
   pdl_trigger();
   // this lane's token of each group of 8; past the last one it is token 0, whose sums there are not stored
   const bf16* xp[NT];
@@ -279,7 +281,7 @@ static int launch_gemv(const GemvArgs& a, bool silu, cudaStream_t st) {
 }
 
 static int linear(const bf16* x, const void* codes, const void* scales, const void* zeros, bf16* out, int64_t M, int64_t N,
-                  int64_t K, int group, int tp, int mode, int epi, cudaStream_t st) {
+                  int64_t K, int group, int tp, int mode, int epi, int flags, cudaStream_t st) {
   const int64_t K_l = mode == QW_GEMM_ROW_REDUCE ? K / tp : K;
   GemvArgs a{};
   const bool silu = epi == QW_EPI_SILU_MUL;
@@ -291,13 +293,14 @@ static int linear(const bf16* x, const void* codes, const void* scales, const vo
   a.i_l = silu ? N / 2 / tp : 0;
   a.tiles = silu ? N / 16 : (N + 15) / 16;
   a.M = int(M);
+  a.early = flags & QW_W4_WEIGHTS_READY;
   a.K = int(K);
   a.pieces = int(K / kPiece);
   a.pieces_l = int(K_l / kPiece);
   const int shards = mode == QW_GEMM_ROW_REDUCE ? tp : 1, nt = int((M + 7) / 8);
   const bool whole = a.pieces_l % 4 == 0;
   if (nt > 8 || (nt > 1 && tc_is_faster(nt, N, K, K_l, silu ? tp : 0, shards)) || (nt > 1 && !whole))
-    return gemm_tc(x, a.w, out, M, N, K, shards, tp, silu, st);
+    return gemm_tc(x, a.w, out, M, N, K, shards, tp, silu, a.early, st);
   if (!whole) return launch_gemv<1, 1, 2, false>(a, silu, st);
   switch (nt) {
     case 1: {
@@ -356,8 +359,9 @@ extern "C" size_t qw_w4_gemm_workspace_size(int64_t M, int64_t N, int64_t K, int
 
 extern "C" int qw_w4_gemm(const void* A, const void* codes, const void* scales, const void* zeros, void* C, int64_t M,
                           int64_t N, int64_t K, int group, int tp, int mode, int epilogue, void* workspace,
-                          size_t workspace_bytes, int dtype, void* stream) {
+                          size_t workspace_bytes, int dtype, int flags, void* stream) {
   if (dtype != QW_BF16) return set_error(QW_ERR_DTYPE, "qw_w4_gemm: dtype %d", dtype);
+  if (flags & ~QW_W4_WEIGHTS_READY) return set_error(QW_ERR_INVALID_ARG, "qw_w4_gemm: flags %d", flags);
   if (M < 0 || N <= 0 || K <= 0 || tp <= 0) return set_error(QW_ERR_INVALID_ARG, "qw_w4_gemm: bad sizes");
   if (mode != QW_GEMM_COLUMN && mode != QW_GEMM_ROW_REDUCE)
     return set_error(QW_ERR_INVALID_ARG, "qw_w4_gemm: mode %d", mode);
@@ -380,7 +384,7 @@ extern "C" int qw_w4_gemm(const void* A, const void* codes, const void* scales, 
   if (need && (!workspace || workspace_bytes < need))
     return set_error(QW_ERR_WORKSPACE, "qw_w4_gemm: workspace of %zu bytes needed", need);
   return w4::linear(static_cast<const bf16*>(A), codes, scales, zeros, static_cast<bf16*>(C), M, N, K, group, tp, mode,
-                    epilogue, static_cast<cudaStream_t>(stream));
+                    epilogue, flags, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t qw_w4_lm_head_workspace_size(int64_t n_out, int64_t V, int64_t H, int tp) {
@@ -391,8 +395,10 @@ extern "C" size_t qw_w4_lm_head_workspace_size(int64_t n_out, int64_t V, int64_t
 
 extern "C" int qw_w4_lm_head(const void* hidden, int64_t T, const int32_t* last_idx, int64_t n_out, const void* codes,
                              const void* scales, const void* zeros, int64_t V, int64_t H, int group, int tp, void* logits,
-                             int64_t* next_tokens, void* workspace, size_t workspace_bytes, int dtype, void* stream) {
+                             int64_t* next_tokens, void* workspace, size_t workspace_bytes, int dtype, int flags,
+                             void* stream) {
   if (dtype != QW_BF16) return set_error(QW_ERR_DTYPE, "qw_w4_lm_head: dtype %d", dtype);
+  if (flags & ~QW_W4_WEIGHTS_READY) return set_error(QW_ERR_INVALID_ARG, "qw_w4_lm_head: flags %d", flags);
   if (T < 0 || n_out < 0 || V <= 0 || H <= 0 || tp <= 0) return set_error(QW_ERR_INVALID_ARG, "qw_w4_lm_head: bad sizes");
   if (V % tp) return set_error(QW_ERR_SHAPE, "qw_w4_lm_head: V=%lld %% tp=%d", (long long)V, tp);
   if (n_out == 0) return QW_OK;
@@ -414,7 +420,7 @@ extern "C" int qw_w4_lm_head(const void* hidden, int64_t T, const int32_t* last_
     x = rows;
   }
   int e = w4::linear(static_cast<const bf16*>(x), codes, scales, zeros, static_cast<bf16*>(logits), n_out, V, H, group, 1,
-                     QW_GEMM_COLUMN, QW_EPI_NONE, st);
+                     QW_GEMM_COLUMN, QW_EPI_NONE, flags, st);
   if (e || !next_tokens) return e;
   if (V % 8 == 0) return launch_argmax<bf16>(logits, n_out, V, next_tokens, st);   // whole 16-byte pieces
   launch_pdl(w4::argmax_kernel, unsigned(n_out), 1024, 0, st, static_cast<const bf16*>(logits), V, next_tokens);

@@ -18,6 +18,7 @@ maths; [SK] AIInfraGuide "3.3 模型骨架与核心算子".
 from __future__ import annotations
 
 import contextlib
+import dataclasses
 from dataclasses import dataclass, field
 from typing import Dict, List, Optional
 
@@ -30,8 +31,40 @@ from . import _lib as L
 # load-time layout (the weight_loader of the parallel Linear family)
 # ----------------------------------------------------------------------------
 
+@dataclass(frozen=True)
+class W4Config:
+    """Linear weights in 4 bits (bf16 models): codes with a scale for each row and `group` columns.
+
+    zeros: a zero point for each group too (asymmetric).  table: the tied embedding / lm_head table as well.
+    """
+    group: int = 128          # 32, 64 or 128; it divides the columns of every shard's rows
+    zeros: bool = False
+    table: bool = True
+
+
+@dataclass
+class W4Weight:
+    """A weight of N stored rows of K columns in 4 bits (the format of qw_w4_quantize); a row split has tp * N rows."""
+    codes: torch.Tensor              # uint8 [N, K/2]
+    scales: torch.Tensor             # bf16 [N, K/group]
+    zeros: Optional[torch.Tensor]    # uint8 [N, K/group]
+    group: int
+
+
+def w4_weight(w: torch.Tensor, c: W4Config) -> W4Weight:
+    """Quantises a bf16 weight [..., K] on its device."""
+    w = w.reshape(-1, w.shape[-1])
+    N, K = w.shape
+    new = lambda cols, dt: torch.empty(N, cols, dtype=dt, device=w.device)  # noqa: E731
+    q = W4Weight(new(K // 2, torch.uint8), new(K // c.group, torch.bfloat16),
+                 new(K // c.group, torch.uint8) if c.zeros else None, c.group)
+    L.w4_quantize(w, c.group, q.codes, q.scales, q.zeros)
+    return q
+
+
 @dataclass
 class LayerParams:
+    # qkv, o, gate_up and down may be W4Weight: the same rows in 4 bits
     qkv: torch.Tensor        # [tp * (nh/tp + 2 nkv/tp) * hd, H]   shard r = [q_r; k_r; v_r]
     o: torch.Tensor          # [tp, H, nh/tp * hd]                 shard r = input columns of its heads
     gate_up: torch.Tensor    # [tp * 2 * I/tp, H]                  shard r = [gate_r; up_r]
@@ -44,7 +77,7 @@ class LayerParams:
 
 @dataclass
 class ModelParams:
-    embed: torch.Tensor      # [V, H]; tied with the lm_head ([SK] §8); shard r = row block r
+    embed: torch.Tensor      # [V, H] (or W4Weight); tied with the lm_head ([SK] §8); shard r = row block r
     layers: List[LayerParams]
     final_norm: torch.Tensor
 
@@ -74,8 +107,19 @@ def shard_layer(shape, ck: Dict[str, torch.Tensor], layer: int, device) -> Layer
                        dev(ck[p + "post_attention_layernorm"]), dev(ck[p + "q_norm"]), dev(ck[p + "k_norm"]))
 
 
-def load_params(shape, seed: int = 0, device="cuda", n_layers: Optional[int] = None, gen_device=None) -> ModelParams:
-    """Random-init parameters of the given shape from the seeded generator."""
+def w4_layer(p: LayerParams, c: W4Config) -> LayerParams:
+    """The layer with its four linear weights in 4 bits."""
+    return dataclasses.replace(p, **{n: w4_weight(getattr(p, n), c) for n in ("qkv", "o", "gate_up", "down")})
+
+
+def w4_params(p: ModelParams, c: W4Config) -> ModelParams:
+    """The parameters with their linear weights, and the tied table, in 4 bits."""
+    return ModelParams(w4_weight(p.embed, c) if c.table else p.embed, [w4_layer(l, c) for l in p.layers], p.final_norm)
+
+
+def load_params(shape, seed: int = 0, device="cuda", n_layers: Optional[int] = None, gen_device=None,
+                w4: Optional[W4Config] = None) -> ModelParams:
+    """Random-init parameters of the given shape from the seeded generator; w4: quantised layer by layer as they load."""
     import seeded_inputs as si
     gen_device = gen_device or device
     nl = shape.n_layers if n_layers is None else n_layers
@@ -85,10 +129,11 @@ def load_params(shape, seed: int = 0, device="cuda", n_layers: Optional[int] = N
         ck = {n: si.checkpoint_tensor(shape, n, seed, gen_device)
               for n in si.weight_names(l) + [f"layer{l}.{x}" for x in
                                              ("input_layernorm", "post_attention_layernorm", "q_norm", "k_norm")]}
-        layers.append(shard_layer(shape, ck, l, device))
-        del ck
+        layer = shard_layer(shape, ck, l, device)
+        layers.append(layer if w4 is None else w4_layer(layer, w4))
+        del ck, layer
     final = si.checkpoint_tensor(shape, "norm", seed, gen_device).to(device)
-    return ModelParams(embed, layers, final)
+    return ModelParams(w4_weight(embed, w4) if w4 is not None and w4.table else embed, layers, final)
 
 
 # ----------------------------------------------------------------------------
@@ -174,7 +219,7 @@ class Qwen3Forward:
         self.m = shape
         self.p = params
         self.device = device
-        dt = params.embed.dtype
+        dt = params.final_norm.dtype
         self.dtype = dt
         H, I, hd = shape.hidden, shape.intermediate, shape.head_dim
         tp = shape.tp
@@ -219,6 +264,12 @@ class Qwen3Forward:
             ws = max(ws, L.attention_decode_kv8_workspace_size(max(max_seqs, 1), max_context, shape.n_heads,
                                                                shape.n_kv_heads), L.ATTENTION_PREFILL_KV8_WORKSPACE_MAX)
         ws = max(ws, L.lm_head_workspace_size(max(max_seqs, 1), shape.vocab, H, tp, dt))
+        if self.w4 or isinstance(params.embed, W4Weight):
+            if dt != torch.bfloat16:
+                raise ValueError("4-bit weights are for bf16 models")
+            for (M, N, K, mode, epi) in self._gemm_shapes(T) + self._gemm_shapes(max(max_seqs, 1)):
+                ws = max(ws, L.w4_gemm_workspace_size(M, N, K, tp, mode, epi))
+            ws = max(ws, L.w4_lm_head_workspace_size(max(max_seqs, 1), shape.vocab, H, tp))
         # completion counters at its start must be zero before the first call
         self.workspace = torch.zeros(max(ws, 256), dtype=torch.uint8, device=device)
         self.scale = hd ** -0.5
@@ -247,6 +298,26 @@ class Qwen3Forward:
         # replace (8 x 2048-token prefill: 21.0 ms fused, 19.1 ms unfused)
         self.fused_prefill = False
 
+    @property
+    def w4(self) -> bool:
+        """The layers' linear weights are in 4 bits."""
+        return len(self.p.layers) > 0 and isinstance(self.p.layers[0].qkv, W4Weight)
+
+    def _linear(self, A, W, C, N, mode, epilogue, stream=None):
+        """One linear layer, over bf16 / f32 or 4-bit weights."""
+        if isinstance(W, W4Weight):
+            L.w4_gemm(A, W.codes, W.scales, W.zeros, C, N, W.group, self.m.tp, mode, epilogue, self.workspace, stream,
+                      weights_ready=True)   # loaded once, as every weight here
+        else:
+            L.gemm(A, W, C, N, self.m.tp, mode, epilogue, self.workspace, stream)
+
+    def _embed(self, ids, out, stream=None):
+        W = self.p.embed
+        if isinstance(W, W4Weight):
+            L.w4_embed_vocab(ids, W.codes, W.scales, W.zeros, W.group, self.m.tp, out, self.err, stream)
+        else:
+            L.embed_vocab(ids, W, self.m.tp, out, self.err, stream)
+
     def _around(self, name: str, layer: int):
         if self.probe is None:
             return contextlib.nullcontext()
@@ -263,7 +334,7 @@ class Qwen3Forward:
         """Prefill: QK-norm + RoPE + KV store as the QKV GEMM's epilogue (bf16,
         head_dim 128, two whole heads of one shard per 256-column tile)."""
         m = self.m
-        return (self.fused_qkv and self.kv8 is None and self.dtype == torch.bfloat16 and m.head_dim == 128
+        return (self.fused_qkv and self.kv8 is None and not self.w4 and self.dtype == torch.bfloat16 and m.head_dim == 128
                 and ((m.n_heads + 2 * m.n_kv_heads) // m.tp) % 2 == 0 and m.hidden % 8 == 0)
 
     def prefill_fusion_ok(self) -> bool:
@@ -272,7 +343,7 @@ class Qwen3Forward:
         RMSNorm in the o_proj and down GEMMs (a row's hidden columns in one
         cluster of 256-column tiles)."""
         m = self.m
-        return (self.fused_prefill and self.kv8 is None and self.dtype == torch.bfloat16 and m.head_dim == 128
+        return (self.fused_prefill and self.kv8 is None and not self.w4 and self.dtype == torch.bfloat16 and m.head_dim == 128
                 and ((m.n_heads + 2 * m.n_kv_heads) // m.tp) % 2 == 0 and m.hidden % 256 == 0
                 and m.hidden <= 2048 and (m.n_heads * m.head_dim // m.tp) % 8 == 0
                 and (m.intermediate // m.tp) % 8 == 0 and len(self.p.layers) > 0)
@@ -314,7 +385,7 @@ class Qwen3Forward:
 
     def norm_fusion_ok(self, T: int) -> bool:
         """Few bf16 tokens: each add+RMSNorm runs as the prologue of the GEMM it feeds."""
-        return self.dtype == torch.bfloat16 and T <= 16 and T <= self.res2.shape[0]
+        return self.dtype == torch.bfloat16 and T <= 16 and T <= self.res2.shape[0] and not self.w4
 
     def _res(self, c: int, T: int):
         """Residual after update c of a decode step (two per layer) when norms are fused."""
@@ -344,7 +415,7 @@ class Qwen3Forward:
                                                   self.k_cache[l], self.v_cache[l], self.q[:T], self.err, stream)
             else:
                 with self._around(f"{ph}.gemm_qkv", l):
-                    L.gemm(y, p.qkv, qkv, self.qkv_width, tp, L.QW_GEMM_COLUMN, L.QW_EPI_NONE, self.workspace, stream)
+                    self._linear(y, p.qkv, qkv, self.qkv_width, L.QW_GEMM_COLUMN, L.QW_EPI_NONE, stream)
         q = self.q[:T]
         attn = self.attn[:T]
         if not decode and self.qkv_epilogue_ok():
@@ -379,7 +450,7 @@ class Qwen3Forward:
                                         ctx.seq_base, ctx.max_seqlen, m.n_heads, m.n_kv_heads, m.head_dim,
                                         self.scale, attn, stream)
         with self._around(f"{ph}.gemm_o", l):
-            L.gemm(attn, p.o, h, m.hidden, tp, L.QW_GEMM_ROW_REDUCE, L.QW_EPI_NONE, self.workspace, stream)
+            self._linear(attn, p.o, h, m.hidden, L.QW_GEMM_ROW_REDUCE, L.QW_EPI_NONE, stream)
         act = self.act[:T]
         if fused:
             # residual update 2l + 1 as the prologue of gate_up + SiluAndMul
@@ -390,10 +461,9 @@ class Qwen3Forward:
             with self._around(f"{ph}.add_rmsnorm", l):
                 L.add_rmsnorm(h, res, res, p.post_ln, m.eps, y, stream)
             with self._around(f"{ph}.gemm_gate_up_silu", l):
-                L.gemm(y, p.gate_up, act, 2 * m.intermediate, tp, L.QW_GEMM_COLUMN, L.QW_EPI_SILU_MUL,
-                       self.workspace, stream)
+                self._linear(y, p.gate_up, act, 2 * m.intermediate, L.QW_GEMM_COLUMN, L.QW_EPI_SILU_MUL, stream)
         with self._around(f"{ph}.gemm_down", l):
-            L.gemm(act, p.down, h, m.hidden, tp, L.QW_GEMM_ROW_REDUCE, L.QW_EPI_NONE, self.workspace, stream)
+            self._linear(act, p.down, h, m.hidden, L.QW_GEMM_ROW_REDUCE, L.QW_EPI_NONE, stream)
 
     def _check_kv8(self, ctx, decode: bool):
         """Refuses a context without the fields that the 8-bit paged cache is addressed by."""
@@ -422,7 +492,7 @@ class Qwen3Forward:
 
     def fused_decode_ok(self, B: int) -> bool:
         m = self.m
-        if not self.fused_decode or self.kv8 is not None or self.dtype != torch.bfloat16 or len(self.p.layers) == 0 or B > self.max_seqs:
+        if not self.fused_decode or self.kv8 is not None or self.w4 or self.dtype != torch.bfloat16 or len(self.p.layers) == 0 or B > self.max_seqs:
             return False
         return L.decode_layers_workspace_size(len(self.p.layers), B, m.hidden, m.n_heads, m.n_kv_heads, m.head_dim,
                                               m.intermediate, m.tp, self.max_context) > 0
@@ -447,7 +517,7 @@ class Qwen3Forward:
         B = ctx.n_tokens
         table, ws = self._fused_state()
         with self._around("decode.embed_vocab", -1):
-            L.embed_vocab(ctx.ids, self.p.embed, m.tp, self.h[:B], self.err, stream)
+            self._embed(ctx.ids, self.h[:B], stream)
         with self._around("decode.layers", -1):
             L.decode_layers(table, len(self.p.layers), self.h[:B], ctx.positions, ctx.slot_mapping, ctx.context_lens,
                             ctx.seq_base, ctx.max_context, m.n_heads, m.n_kv_heads, m.head_dim, m.intermediate, m.tp,
@@ -466,7 +536,7 @@ class Qwen3Forward:
             return self._decode_fused(ctx, stream)
         if hidden_in is None:
             with self._around(f"{'decode' if decode else 'prefill'}.embed_vocab", -1):
-                L.embed_vocab(ctx.ids, self.p.embed, m.tp, self.h[:T], self.err, stream)
+                self._embed(ctx.ids, self.h[:T], stream)
         else:
             self.h[:T].copy_(hidden_in)
         nl = len(self.p.layers)
@@ -492,7 +562,12 @@ class Qwen3Forward:
         logits = self.logits[:n_out]
         nt = self.next_tokens[:n_out]
         with self._around("lm_head", -1):
-            L.lm_head(hidden, last_idx, n_out, self.p.embed, self.m.tp, logits, nt, self.workspace, stream)
+            W = self.p.embed
+            if isinstance(W, W4Weight):
+                L.w4_lm_head(hidden, last_idx, n_out, W.codes, W.scales, W.zeros, W.group, self.m.tp, logits, nt,
+                             self.workspace, stream, weights_ready=True)
+            else:
+                L.lm_head(hidden, last_idx, n_out, W, self.m.tp, logits, nt, self.workspace, stream)
         return logits, nt
 
     def prefill(self, ctx: PrefillContext, stream=None):

@@ -421,13 +421,13 @@ def test_mlp_from_quantised_weights(L, M):
     ws = torch.zeros(max(L.w4_lm_head_workspace_size(M, V, H, tp), L.w4_gemm_workspace_size(M, 2 * I, H, tp, COL, SILU),
                          L.w4_gemm_workspace_size(M, H, I, tp, ROW, NONE)), dtype=torch.uint8, device=dev)
 
-    def step():
+    def step(ready=True):
         L.w4_embed_vocab(ids, *q[0], G, tp, x)
-        L.w4_gemm(x, *q[1], act, 2 * I, G, tp, COL, SILU, ws)
-        L.w4_gemm(act, *q[2], y, H, G, tp, ROW, NONE, ws)
-        L.w4_lm_head(y, None, M, *q[0], G, tp, logits, tok, ws)
+        L.w4_gemm(x, *q[1], act, 2 * I, G, tp, COL, SILU, ws, weights_ready=ready)
+        L.w4_gemm(act, *q[2], y, H, G, tp, ROW, NONE, ws, weights_ready=ready)
+        L.w4_lm_head(y, None, M, *q[0], G, tp, logits, tok, ws, weights_ready=ready)
 
-    step()
+    step(False)
     sync_ok(L)
     assert torch.equal(x, vals[0][ids])
     y1, e1 = product(x.double().cpu(), vals[1].double().cpu())
@@ -454,3 +454,45 @@ def test_mlp_from_quantised_weights(L, M):
         sync_ok(L)
         assert all(torch.equal(a, b) for a, b in zip(want, (act, y, logits, tok)))
     assert len(first) == 4
+
+
+@pytest.mark.parametrize("M", [1, 12, 100])
+def test_weights_written_just_before(L, M):
+    """Quantised and multiplied in turn on one stream, without the statement that the weights were there."""
+    N, K, G = 512, 1024, 64
+    x = torch.randn(M, K, generator=gen(M)).bfloat16().cuda()
+    ws = [(0.1 * torch.randn(N, K, generator=gen(i))).bfloat16().cuda() for i in range(6)]
+    c, s, z = (torch.empty(N, k, dtype=d, device="cuda") for k, d in ((K // 2, torch.uint8), (K // G, torch.bfloat16),
+                                                                     (K // G, torch.uint8)))
+    want = []
+    for w in ws:
+        L.w4_quantize(w, G, c, s, z)
+        torch.cuda.synchronize()
+        want.append(run_gemm(L, x, c, s, z, N, G, 1, COL, NONE))
+        torch.cuda.synchronize()
+    outs = [torch.empty(M, N, dtype=torch.bfloat16, device="cuda") for _ in ws]
+    for _ in range(20):
+        for w, o in zip(ws, outs):
+            L.w4_quantize(w, G, c, s, z)
+            L.w4_gemm(x, c, s, z, o, N, G)
+        sync_ok(L)
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("M", [2, 40, 200])
+def test_two_streams_and_a_wide_batch_at_once(L, M):
+    """Calls side by side on two streams, each into its own output, give what they give alone."""
+    N, K = 1024, 2048
+    c, s, z, _ = matrix(N, K, 128, True, seed=3)
+    xs = [torch.randn(M, K, generator=gen(i)).bfloat16().cuda() for i in range(2)]
+    want = [run_gemm(L, x, c, s, z, N, 128, 1, COL, NONE) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[torch.empty(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(10)] for _ in xs]
+    torch.cuda.synchronize()
+    for i in range(10):
+        for st, x, o in zip(streams, xs, outs):
+            L.w4_gemm(x, c, s, z, o[i], N, 128, stream=st)
+    sync_ok(L)
+    for o, w in zip(outs, want):
+        assert all(torch.equal(a, w) for a in o)

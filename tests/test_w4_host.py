@@ -16,9 +16,9 @@ QUANT = dict(w=FAKE, N=64, K=256, group=64, codes=FAKE, scales=FAKE, zeros=None,
 EMBED = dict(ids=FAKE, T=4, codes=FAKE, scales=FAKE, zeros=None, V=64, H=256, group=64, tp=1, out=FAKE, err=None,
              dt=L.QW_BF16, st=None)
 GEMM = dict(A=FAKE, codes=FAKE, scales=FAKE, zeros=None, C=FAKE, M=4, N=64, K=256, group=64, tp=1, mode=COL, epi=0, ws=FAKE,
-            wsb=1 << 40, dt=L.QW_BF16, st=None)
+            wsb=1 << 40, dt=L.QW_BF16, flags=0, st=None)
 HEAD = dict(hidden=FAKE, T=8, last=FAKE, n=4, codes=FAKE, scales=FAKE, zeros=None, V=64, H=256, group=64, tp=1, logits=FAKE,
-            tok=FAKE, ws=FAKE, wsb=1 << 40, dt=L.QW_BF16, st=None)
+            tok=FAKE, ws=FAKE, wsb=1 << 40, dt=L.QW_BF16, flags=0, st=None)
 ENTRY = {"quantize": ("qw_w4_quantize", QUANT), "embed": ("qw_w4_embed_vocab", EMBED), "gemm": ("qw_w4_gemm", GEMM),
          "head": ("qw_w4_lm_head", HEAD)}
 WIDTH = {"quantize": "K", "embed": "H", "gemm": "K", "head": "H"}
@@ -58,7 +58,7 @@ def test_weight_refusals(lib, op, kw, want):
     ("gemm", dict(mode=2), ARG), ("gemm", dict(epi=2), ARG), ("gemm", dict(epi=SILU, mode=ROW), ARG),
     ("gemm", dict(tp=0), ARG), ("gemm", dict(tp=3), SHAPE), ("gemm", dict(tp=3, mode=ROW), SHAPE),
     ("gemm", dict(tp=8, mode=ROW), SHAPE), ("gemm", dict(tp=2, epi=SILU, N=48), SHAPE), ("gemm", dict(epi=SILU, N=24), SHAPE),
-    ("gemm", dict(N=1 << 31), SHAPE),
+    ("gemm", dict(N=1 << 31), SHAPE), ("gemm", dict(flags=2), ARG), ("head", dict(flags=-1), ARG),
     ("head", dict(n=-1), ARG), ("head", dict(n=0), OK), ("head", dict(T=-1), ARG), ("head", dict(last=None, n=9), SHAPE),
     ("head", dict(hidden=None), ARG), ("head", dict(hidden=ODD), ARG), ("head", dict(logits=None), ARG),
     ("head", dict(logits=ODD), ARG), ("head", dict(tp=3), SHAPE), ("head", dict(ws=None), WS), ("head", dict(wsb=1024), WS),
