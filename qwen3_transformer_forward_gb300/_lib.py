@@ -483,15 +483,16 @@ def _w4_check(codes, scales, zeros, group, rows, columns):
     if codes.dtype is not torch.uint8 or scales.dtype is not torch.bfloat16:
         raise QwError(QW_ERR_DTYPE, f"codes must be uint8 and scales bfloat16, not {codes.dtype} and {scales.dtype}")
     per_row = columns // group if group > 0 else 0
-    groups = rows * per_row
-    if (codes.numel() * 2 != rows * columns or codes.shape[-1] * 2 != columns or scales.numel() != groups
-            or scales.shape[-1] != per_row):
-        raise QwError(QW_ERR_SHAPE, f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} are not {rows} rows of "
-                                    f"{columns} columns in groups of {group}")
+    # (a row split may come as [tp, N, ..]: the last dimension and the number of elements say as much as the shape)
+    if codes.shape != (rows, columns // 2) or scales.shape != (rows, per_row):
+        if (codes.numel() * 2 != rows * columns or codes.shape[-1] * 2 != columns or scales.numel() != rows * per_row
+                or scales.shape[-1] != per_row):
+            raise QwError(QW_ERR_SHAPE, f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} are not {rows} rows of "
+                                        f"{columns} columns in groups of {group}")
     if zeros is not None:
         if zeros.dtype is not torch.uint8:
             raise QwError(QW_ERR_DTYPE, f"zeros must be uint8, not {zeros.dtype}")
-        if zeros.numel() != groups or zeros.shape[-1] != per_row:
+        if zeros.numel() != rows * per_row or zeros.shape[-1] != per_row:
             raise QwError(QW_ERR_SHAPE, f"zeros {tuple(zeros.shape)} are not {rows} rows of {per_row} groups")
 
 
@@ -536,17 +537,22 @@ def w4_gemm(A, codes, scales, zeros, C_out, N, group, tp=1, mode=QW_GEMM_COLUMN,
     weights_ready: the previous kernel on the stream, and those that may still run beside it, write none of the weights
     (see QW_W4_WEIGHTS_READY in qw.h)."""
     M, K = A.shape
-    shards = tp if mode == QW_GEMM_ROW_REDUCE else 1
-    if tp > 0:
-        _w4_check(codes, scales, zeros, group, shards * N, K // shards)
-    if C_out.dtype is not A.dtype:
-        raise QwError(QW_ERR_DTYPE, f"the output's type {C_out.dtype} is not the input's, {A.dtype}")
+    if mode != QW_GEMM_ROW_REDUCE:
+        _w4_check(codes, scales, zeros, group, N, K)
+    elif tp > 0:
+        _w4_check(codes, scales, zeros, group, tp * N, K // tp)
+    dtype = A.dtype
+    if C_out.dtype is not dtype:
+        raise QwError(QW_ERR_DTYPE, f"the output's type {C_out.dtype} is not the input's, {dtype}")
     if C_out.numel() != M * (N // 2 if epilogue == QW_EPI_SILU_MUL else N):
         raise QwError(QW_ERR_SHAPE, f"output {tuple(C_out.shape)} for {M} tokens of {N} features")
-    _check(load().qw_w4_gemm(
+    rc = (_lib or load()).qw_w4_gemm(
         _dev_ptr(A, "A"), _dev_ptr(codes, "codes"), _dev_ptr(scales, "scales"), _dev_ptr(zeros, "zeros"),
-        _dev_ptr(C_out, "C"), M, N, K, group, tp, mode, epilogue, _dev_ptr(workspace, "workspace"), _w4_bytes(workspace),
-        dtype_code(A.dtype), QW_W4_WEIGHTS_READY if weights_ready else 0, _stream(stream)))
+        _dev_ptr(C_out, "C"), M, N, K, group, tp, mode, epilogue, _dev_ptr(workspace, "workspace"),
+        0 if workspace is None else _w4_bytes(workspace), QW_BF16 if dtype is torch.bfloat16 else dtype_code(dtype),
+        QW_W4_WEIGHTS_READY if weights_ready else 0, _stream(stream))
+    if rc != QW_OK:
+        _check(rc)
 
 
 def w4_lm_head_workspace_size(n_out, V, H, tp) -> int:
