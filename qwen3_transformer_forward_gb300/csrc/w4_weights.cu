@@ -19,6 +19,20 @@ namespace w4 {
 // ---------------------------------------------------------------------------
 constexpr int kQuant = 4;
 constexpr float kSnap = 6144.0f, kInt = 12582912.0f;   // 1.5 * 2^12, 1.5 * 2^23
+constexpr uint32_t kIntBits = 0x4b400000u;              // kInt's
+constexpr uint32_t int_bits_of_word() {                 // the sum of kIntBits at the eight places, modulo 2^32
+  uint32_t sum = 0;
+  for (int p = 0; p < 32; p += 4) sum += kIntBits << p;
+  return sum;
+}
+
+// bf16(x / n) in fp32, inv = 1 / n rounded: x * inv differs from x / n by less than 4 units in its last place, so the two
+// round alike unless x * inv lies within 8 of a midpoint between two bf16 numbers.
+__device__ __forceinline__ float quotient_bf16(float x, float n, float inv) {
+  float t = x * inv;
+  if (((__float_as_uint(t) - 0x7ff8u) & 0xffffu) <= 16u) t = __fdiv_rn(x, n);
+  return round_t<bf16>(t);
+}
 
 // any group: with infinities, NaN, or so small that 1 / s is no normal number
 template <bool ZEROS>
@@ -89,18 +103,16 @@ __global__ void __launch_bounds__(256) quantize_kernel(const uint4* __restrict__
       const uint32_t a = *reinterpret_cast<uint32_t*>(&mx), b = *reinterpret_cast<uint32_t*>(&mn);
       hi = fmaxf(bf16_lo(a), bf16_hi(a));
       lo = fminf(bf16_lo(b), bf16_hi(b));
-      const bool bad = ((a & 0x7f80u) == 0x7f80u) || ((a & 0x7f800000u) == 0x7f800000u) || ((b & 0x7f80u) == 0x7f80u) ||
-                       ((b & 0x7f800000u) == 0x7f800000u);
-      const float top = __fdiv_rn(__fsub_rn(hi, lo), 15.0f);
-      s = round_t<bf16>(top);
-      any = bad || !(top < 0x1p120f);
+      // a sum of magnitudes: neither small nor a number if one of them is NaN or infinite
+      any = !((bf16_lo(a) + bf16_hi(a)) - (bf16_lo(b) + bf16_hi(b)) < 0x1p120f);
+      s = quotient_bf16(__fsub_rn(hi, lo), 15.0f, 1.0f / 15.0f);
     } else {
       uint32_t m = __vmaxu2(__vmaxu2(p[0] & 0x7fff7fffu, p[1] & 0x7fff7fffu), __vmaxu2(p[2] & 0x7fff7fffu, p[3] & 0x7fff7fffu));
       for (int o = 1; o < lanes; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
       const uint32_t top = max(m >> 16, m & 0xffffu);   // |w| as bits: their order is that of the values
       any = top >= 0x7f80u;
       hi = __uint_as_float(top << 16);
-      s = round_t<bf16>(__fdiv_rn(hi, 7.0f));
+      s = quotient_bf16(hi, 7.0f, 1.0f / 7.0f);
     }
     any = any || s < 0x1p-100f;   // also 0
     uint32_t word;
@@ -110,13 +122,12 @@ __global__ void __launch_bounds__(256) quantize_kernel(const uint4* __restrict__
       const float r = __fdividef(1.0f, s);
       if (ZEROS) z = __fadd_rn(__fadd_rn(__fmaf_rn(-lo, r, kSnap), kInt - kSnap), -kInt);
       const float top = kSnap + 15.0f - z;
-      word = ZEROS ? uint32_t(int(z)) * 0x11111111u : 0x88888888u;
+      word = (ZEROS ? uint32_t(int(z)) * 0x11111111u : 0x88888888u) - int_bits_of_word();
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         float t = __fmaf_rn(e & 1 ? bf16_hi(p[e / 2]) : bf16_lo(p[e / 2]), r, kSnap);
         if (ZEROS) t = fminf(t, top);
-        const uint32_t q = __float_as_uint(__fadd_rn(t, kInt - kSnap));   // 0x4b400000 + rne(w / s)
-        word += (q - 0x4b400000u) << (4 * ((e & 1) * 4 + e / 2));
+        word += __float_as_uint(__fadd_rn(t, kInt - kSnap)) << (4 * ((e & 1) * 4 + e / 2));   // kIntBits + rne(w / s)
       }
     }
     const int64_t v = v0 + 256 * i;
