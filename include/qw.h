@@ -637,7 +637,7 @@ int qw_w4_embed_vocab(const int64_t* ids, int64_t T, const void* codes, const vo
  *     C [M, N/2] = silu(gate) * up is formed from the fp32 sums.
  *   QW_GEMM_ROW_REDUCE: codes [tp, N, K/tp/2], scales and zeros
  *     [tp, N, K/tp/group]; any N.
- * Any M below 2^21.  A and C 16-byte aligned.
+ * Any M below 2^21.  A and C 16-byte aligned; C must not overlap A.
  * flags: 0, or QW_W4_WEIGHTS_READY: the caller states that codes, scales and
  *   zeros were complete before the kernel enqueued just before this call
  *   started (weights that were loaded once).  They are then read before that

@@ -5,6 +5,17 @@
 // copied by TMA.  Two CTAs (cta_group::2) share a tile of 256 weight rows: each decodes
 // 128 of them and holds half of the tokens, so that the tokens cross L2 and each shared
 // memory once for 256 rows.
+//
+// Warps of a CTA: 0 copies tokens, 2 codes, 1 (of the pair's rank 0) issues the MMAs, from 4 on sets of four decode (a
+// thread a weight row), the last four store.  TMEM: two accumulators of up to 192 tokens (128 in the narrow form) and a
+// ring of decoded weights, two steps of 128 columns (four).  What a step of 192 tokens costs, in cycles: its MMAs 770,
+// decoding about 400 of the sub-partition's pipes, the MMA warp's waits and issue about 450; so the tensor pipe leads
+// (N of 192 rather than 256 leaves TMEM for the second accumulator: stores overlap the next tile's MMAs).
+// 16384 x 12288 x 2048 with SiluAndMul: 480-496 us, 1.66-1.72 PFLOP/s, the rate that a large library product sustains
+// under the power limit; 4096 x 12288 x 2048: 121 us, 1.70 PFLOP/s.  With few tokens the decoding sets' latency leads:
+// about 365 cycles for 128 rows x 64 columns against 190 of memory (128 x 28672 x 8192 61 us; 65 x 151936 x 1024 36 us).
+// One CTA for itself with 192 tokens ran at 793 us (tokens' traffic twice), the MMAs issued by one lane in a branch at
+// 1162, arrivals at the other CTA's barriers that release all memory at 887 against 637.
 #include <algorithm>
 #include <type_traits>
 

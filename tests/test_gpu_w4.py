@@ -496,3 +496,79 @@ def test_two_streams_and_a_wide_batch_at_once(L, M):
     sync_ok(L)
     for o, w in zip(outs, want):
         assert all(torch.equal(a, w) for a in o)
+
+
+@pytest.mark.parametrize("M", [1, 9, 70, 200])
+def test_offsets_past_2_to_31(L, M):
+    """A matrix of 2.4 GB of codes: its last rows, and its last row as an embedding."""
+    N, K, G, tail = 300000, 16384, 128, 40
+    c, s, z, w = matrix(tail, K, G, True, seed=2)
+    codes = torch.zeros(N, K // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(N, K // G, dtype=torch.bfloat16, device="cuda")
+    zeros = torch.full((N, K // G), 3, dtype=torch.uint8, device="cuda")
+    codes[-tail:], scales[-tail:], zeros[-tail:] = c, s, z
+    x = torch.randn(M, K, generator=gen(M)).bfloat16()
+    out = run_gemm(L, x.cuda(), codes, scales, zeros, N, G, 1, COL, NONE)
+    row = torch.empty(2, K, dtype=torch.bfloat16, device="cuda")
+    L.w4_embed_vocab(torch.tensor([N - 1, 5], device="cuda"), codes, scales, zeros, G, 1, row)
+    sync_ok(L)
+    near(out[:, -tail:], *product(x.double(), w), M)
+    assert (out[:, :-tail] == 0).all()
+    assert torch.equal(row[0].double().cpu(), w[-1]) and (row[1] == 0).all()
+
+
+@pytest.mark.parametrize("M,N,K,group,tp,mode,epi", [(1, 1, 32, 32, 1, COL, NONE), (300, 1, 64, 32, 2, ROW, NONE),
+                                                     (16, 3, 128, 128, 1, COL, NONE), (129, 16, 32, 32, 1, COL, SILU),
+                                                     (40, 16, 256, 128, 1, COL, SILU), (5000, 32, 128, 64, 2, COL, SILU)])
+def test_gemm_smallest(L, M, N, K, group, tp, mode, epi):
+    check_gemm(L, M, N, K, group, True, tp, mode, epi)
+
+
+@pytest.mark.parametrize("M", [1, 6, 13, 33, 64, 140])
+def test_gemm_drawn_sizes(L, M):
+    """Sizes from all over the range, every kernel choice among them."""
+    import random
+    rng = random.Random(M)
+    for _ in range(6):
+        group, tp = rng.choice([32, 64, 128]), rng.choice([1, 2, 3])
+        mode, epi = rng.choice([(COL, NONE), (ROW, NONE), (COL, SILU)])
+        N = (16 * tp if epi else tp) * rng.randint(1, 120)
+        K = group * tp * rng.randint(1, 1500 // group)
+        check_gemm(L, M, N, K, group, rng.random() < 0.5, tp, mode, epi, seed=rng.randint(1, 99))
+
+
+def test_replayed_graphs_side_by_side(L):
+    """Two captured graphs over the same weights, replayed in turn and on two streams at once."""
+    N, K, V = 768, 512, 1000
+    c, s, z, _ = matrix(N, K, 64, True)
+    tc, ts, _, _ = matrix(V, N, 64, False)
+    runs = []
+    for M in (4, 150):
+        x = torch.randn(M, K, generator=gen(M)).bfloat16().cuda()
+        y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+        logits = torch.empty(M, V, dtype=torch.bfloat16, device="cuda")
+        tok = torch.empty(M, dtype=torch.int64, device="cuda")
+        last = torch.arange(M - 1, -1, -1, dtype=torch.int32, device="cuda")
+        ws = torch.zeros(L.w4_lm_head_workspace_size(M, V, N, 1), dtype=torch.uint8, device="cuda")
+
+        def step():
+            L.w4_gemm(x, c, s, z, y, N, 64, weights_ready=True)
+            L.w4_lm_head(y, last, M, tc, ts, None, 64, 1, logits, tok, ws, weights_ready=True)
+        step()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (y, logits, tok)]
+        st = torch.cuda.Stream()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(st), torch.cuda.graph(graph, stream=st):
+            step()
+        runs.append((graph, st, (y, logits, tok), want, (x, last, ws, step)))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for graph, st, outs, _, _ in runs:
+            with torch.cuda.stream(st):
+                for o in outs:
+                    o.zero_()
+                graph.replay()
+        sync_ok(L)
+        for _, _, outs, want, _ in runs:
+            assert all(torch.equal(a, b) for a, b in zip(outs, want))
