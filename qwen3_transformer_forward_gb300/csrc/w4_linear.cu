@@ -5,8 +5,8 @@
 // added over the warps of a row tile in shared memory, in slice order.
 // Bound: an MMA occupies an SM sub-partition for 16 cycles whatever the number of live tokens, so that a chunk of 16 rows
 // x 128 columns cannot take less than 256 of its cycles; decoding takes 128 of the half-rate bf16 pipe and 112 of the
-// integer pipe beside it.  1 x 28672 x 8192 (117 MB of codes): 28.4 us, 4.3 TB/s, against 25.4 us for its MMAs and 17.9 for
-// its bytes; 8 x 151936 x 1024: 25.4 us against 16.8 and 12.6; 1 x 4096 x 1024: 2.4 us in a graph, launch and latency.
+// integer pipe beside it.  1 x 28672 x 8192 (117 MB of codes): 30 us, 4.0 TB/s, against 25.4 us for its MMAs and 17.9 for
+// its bytes; 8 x 151936 x 1024: 26.3 us against 16.8 and 12.6; 1 x 4096 x 1024: 2.4 us in a graph, launch and latency.
 #include "w4.cuh"
 
 namespace qw {
@@ -246,10 +246,10 @@ __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(GemvArgs a) {
   }
 }
 
-// warps that share a unit of row tiles: up to 8, while there are no more than 32 such warps an SM
-static int gemv_split(int64_t units, int chunks) {
+// warps that share a unit of row tiles: up to 8, while the CTAs run at once (`resident` of them on an SM)
+static int gemv_split(int64_t units, int chunks, int resident) {
   int split = kWarps;
-  while (split > 1 && (split > chunks || units * split > 152 * 32)) split >>= 1;
+  while (split > 1 && (split > chunks || units * split > 152 * kWarps * int64_t(resident))) split >>= 1;
   return split;
 }
 
@@ -274,7 +274,11 @@ static int launch_gemv(GemvArgs a, cudaStream_t st) {
   }
   const int chunks = (a.pieces + 3) / 4;
   const int64_t units = (a.tiles + R - 1) / R;
-  a.split = gemv_split(units, chunks);
+  static const int resident = [&] {
+    int n = 0;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kWarps * 32, smem) == cudaSuccess && n > 0 ? n : 1;
+  }();
+  a.split = gemv_split(units, chunks, resident);
   const int per_cta = kWarps / a.split;
   const dim3 grid(unsigned((units + per_cta - 1) / per_cta), unsigned((a.M + NT * 8 - 1) / (NT * 8)));
   launch_pdl(kern, grid, kWarps * 32, smem, st, a);
@@ -312,11 +316,13 @@ static int linear(const bf16* x, const void* codes, const void* scales, const vo
   if (!whole) return launch_gemv<1, 1, 2, false>(a, silu, st);
   switch (nt) {
     case 1: {
-      // Two row tiles a warp halve the tokens' traffic through L1 (8 x 16 lines a load), one tile leaves more warps:
-      // 4 x 8192 x 8192 18.4 us with one, 11.1 with two, 8 x 151936 x 1024 30.0 and 25.6; 8 x 12288 x 2048, where a
-      // warp has two chunks, 7.3 and 8.7; 1 x 28672 x 8192 29.5 and 36.5.
-      const int chunks = a.pieces / 4, split = gemv_split(a.tiles, chunks);
-      return M > 2 && chunks >= 4 * split ? launch_gemv<1, 2, 2, true>(a, silu, st) : launch_gemv<1, 1, 4, true>(a, silu, st);
+      // Two row tiles a warp halve the tokens' traffic through L1 (8 x 16 lines a load), one tile leaves more warps and
+      // shorter ones; four chunks in flight pay only where a warp has many.  us with one tile and 2 or 4 chunks, two and 2:
+      // 8 x 151936 x 1024 29.3 / 31.1 / 26.3, 4 x 8192 x 8192 14.2 / 18.7 / 12.3, 1 x 28672 x 8192 38.0 / 30.2 / 35.5,
+      // 1 x 4096 x 4096 6.1 / 7.0 / 6.2, 8 x 1024 x 2048 2.6 / 2.7 / 3.2, 1 x 4096 x 1024 2.5 / 2.9 / 2.5.
+      const int chunks = a.pieces / 4, each = chunks / gemv_split(a.tiles, chunks, 3);
+      if (M > 2 && each >= 4) return launch_gemv<1, 2, 2, true>(a, silu, st);
+      return each >= 16 ? launch_gemv<1, 1, 4, true>(a, silu, st) : launch_gemv<1, 1, 2, true>(a, silu, st);
     }
     case 2: return launch_gemv<2, 2, 2, true>(a, silu, st);
     case 3: return launch_gemv<3, 2, 2, true>(a, silu, st);
