@@ -613,7 +613,7 @@ size_t qw_sample_workspace_size(int64_t B, int64_t V);
  * qw_w4_quantize: codes, scales and zeros of a matrix w bf16 [N, K], rounding
  * to nearest even throughout.  For each row and group, over its finite weights:
  *   zeros NULL: s = bf16(max|w| / 7);  n = clamp(round(w / s), -8, 7) + 8
- *   zeros:      lo = min(w, 0), hi = max(w, 0), s = bf16((hi - lo) / 15),
+ *   zeros:      lo = min(w, 0), hi = max(w, 0), s = bf16((hi - lo) / 15) (hi - lo in fp32),
  *               z = min(round(-lo / s), 15), n = clamp(round(w / s) + z, 0, 15)
  * where s is 0, w / 0 counts as w / 1.  NaN counts as 0, an infinity becomes the
  * largest code of its sign.  A row split W [tp, N, K/tp] (qw_gemm) is quantised

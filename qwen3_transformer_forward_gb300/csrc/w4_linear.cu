@@ -26,7 +26,7 @@ int gemm_tc(const bf16* x, const Weights& w, bf16* out, int64_t M, int64_t N, in
 int64_t tc_steps(int64_t N, int64_t K_l, int silu_shards, int shards);
 
 struct GemvArgs {
-  const bf16* x;         // [M, K]
+  const bf16* x;         // [M, K], at most 8 NT tokens
   bf16* out;             // [M, ldc]
   Weights w;             // of one shard's rows
   int64_t rows;          // N: rows of a shard (row split), of the matrix (column)
@@ -58,9 +58,9 @@ constexpr size_t gemv_warp_smem(int nt, int r, int depth) {
 // A warp takes R tiles of 16 weight rows and every split-th chunk of 128 columns; lane (g, t) = (lane / 4,
 // lane % 4) holds the 32 columns of piece t of rows g and g + 8.  The k index of an MMA may be any
 // permutation that weights and tokens share, so a lane's own columns are its k values: no shuffles.
-// The codes of DEPTH chunks are in flight at once, the first ones ahead of the programmatic wait (QW_W4_WEIGHTS_READY): each lane copies
-// asynchronously to shared memory what it reads there itself, so that the depth costs no registers and nothing waits
-// for another lane.
+// The codes of DEPTH chunks are in flight at once, the first ones ahead of the programmatic wait
+// (QW_W4_WEIGHTS_READY): each lane copies asynchronously to shared memory what it reads there itself, so that the depth
+// costs no registers and nothing waits for another lane.
 // WHOLE: a shard's columns are whole chunks, so that nothing in the loop has a condition of its own lane.
 template <int NT, int R, int DEPTH, bool SILU, bool ZEROS, bool WHOLE>
 __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(GemvArgs a) {
@@ -72,7 +72,6 @@ __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(GemvArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int per_cta = kWarps / a.split, sl = warp % a.split;
   const int64_t tile0 = int64_t(blockIdx.x) * per_cta * R, tile = tile0 + warp / a.split * R;
-  const int m0 = blockIdx.y * (NT * 8);
   const uint32_t magic = code_magic();
   // this lane's piece within its shard, pieces from it to the end of K, pieces to the next one
   int lu = 4 * sl + t, left = a.pieces - lu;
@@ -157,7 +156,7 @@ __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(GemvArgs a) {
   const bf16* xp[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const int tok = m0 + n * 8 + g;
+    const int tok = n * 8 + g;
     xp[n] = a.x + int64_t(tok < a.M ? tok : 0) * a.K + (4 * sl + t) * kPiece;
   }
   for (int u0 = 4 * sl; u0 < a.pieces; u0 += advance * DEPTH) {
@@ -230,7 +229,7 @@ __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(GemvArgs a) {
     }
   __syncthreads();
   constexpr int out_rows = SILU ? 8 : 16;   // of a tile
-  const int total = per_cta * R * out_rows, live = min(NT * 8, a.M - m0);
+  const int total = per_cta * R * out_rows, live = a.M;
   for (int e = threadIdx.x; e < total * live; e += kWarps * 32) {
     const int j = e % total, n = e / total, lt = j / out_rows, r = j % out_rows;
     const int64_t o = (tile0 + lt) * out_rows + r;
@@ -242,7 +241,7 @@ __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(GemvArgs a) {
       if (SILU) up += sum_at(w, row + 8, n);
     }
     if (SILU) v = __fdividef(v, 1.0f + __expf(-v)) * up;
-    a.out[int64_t(m0 + n) * a.ldc + o] = __float2bfloat16_rn(v);
+    a.out[int64_t(n) * a.ldc + o] = __float2bfloat16_rn(v);
   }
 }
 
@@ -280,7 +279,7 @@ static int launch_gemv(GemvArgs a, cudaStream_t st) {
   }();
   a.split = gemv_split(units, chunks, resident);
   const int per_cta = kWarps / a.split;
-  const dim3 grid(unsigned((units + per_cta - 1) / per_cta), unsigned((a.M + NT * 8 - 1) / (NT * 8)));
+  const dim3 grid(unsigned((units + per_cta - 1) / per_cta));
   launch_pdl(kern, grid, kWarps * 32, smem, st, a);
   return check_launch("w4 gemv");
 }
