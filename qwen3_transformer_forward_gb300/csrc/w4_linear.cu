@@ -6,7 +6,7 @@
 // Bound: an MMA occupies an SM sub-partition for 16 cycles whatever the number of live tokens, so that a chunk of 16 rows
 // x 128 columns cannot take less than 256 of its cycles; decoding takes 128 of the half-rate bf16 pipe and 112 of the
 // integer pipe beside it.  1 x 28672 x 8192 (117 MB of codes): 30 us, 4.0 TB/s, against 25.4 us for its MMAs and 17.9 for
-// its bytes; 8 x 151936 x 1024: 26.3 us against 16.8 and 12.6; 1 x 4096 x 1024: 2.4 us in a graph, launch and latency.
+// its bytes; 8 x 151936 x 1024: 24.9 us against 16.8 and 12.6; 1 x 4096 x 1024: 2.4 us in a graph, launch and latency.
 #include "w4.cuh"
 
 namespace qw {
@@ -62,7 +62,10 @@ constexpr size_t gemv_warp_smem(int nt, int r, int depth) {
 // (QW_W4_WEIGHTS_READY): each lane copies asynchronously to shared memory what it reads there itself, so that the depth
 // costs no registers and nothing waits for another lane.
 // WHOLE: a shard's columns are whole chunks, so that nothing in the loop has a condition of its own lane.
-template <int NT, int R, int DEPTH, bool SILU, bool ZEROS, bool WHOLE>
+// XS: the tokens lie in shared memory behind the rings, 16 bytes (8 columns, word i of a piece) of lane (g, t) at
+// [chunk][n][i][lane]: a read has no bank conflict, while a load of 8 tokens from memory touches 16 lines.  For warps
+// that walk through all of K (split 1), which all read them.
+template <int NT, int R, int DEPTH, bool SILU, bool ZEROS, bool WHOLE, bool XS>
 __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(GemvArgs a) {
   extern __shared__ __align__(16) uint8_t gemv_dyn[];
   constexpr size_t WARP_SMEM = gemv_warp_smem(NT, R, DEPTH);
@@ -159,6 +162,17 @@ __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(GemvArgs a) {
     const int tok = n * 8 + g;
     xp[n] = a.x + int64_t(tok < a.M ? tok : 0) * a.K + (4 * sl + t) * kPiece;
   }
+  const uint32_t xsm = smem_u32(gemv_dyn) + uint32_t(kWarps * WARP_SMEM);
+  if (XS) {
+    for (int e = threadIdx.x; e < a.pieces / 4 * NT * 128; e += kWarps * 32) {
+      const int tok = (e >> 7) % NT * 8 + ((e >> 2) & 7), k = (e >> 7) / NT * 128 + (e & 3) * 32 + ((e >> 5) & 3) * 8;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (tok < a.M) v = *reinterpret_cast<const uint4*>(a.x + int64_t(tok) * a.K + k);
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(xsm + uint32_t(e) * 16u), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                   : "memory");
+    }
+    __syncthreads();
+  }
   for (int u0 = 4 * sl; u0 < a.pieces; u0 += advance * DEPTH) {
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
@@ -169,11 +183,18 @@ __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(GemvArgs a) {
       auto load_x = [&](int i) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+          if (XS) {
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(x[i][n].x), "=r"(x[i][n].y), "=r"(x[i][n].z), "=r"(x[i][n].w)
+                         : "r"(xsm + uint32_t((((u >> 2) * NT + n) * 4 + i) * 32 + lane) * 16u)
+                         : "memory");
+            continue;
+          }
           if (!WHOLE) x[i][n] = make_uint4(0, 0, 0, 0);
           if (in) x[i][n] = __ldg(reinterpret_cast<const uint4*>(xp[n] + 8 * i));
         }
       };
-      constexpr int AHEAD = NT <= 2 ? 4 : NT <= 6 ? 2 : 1;   // words of tokens in flight
+      constexpr int AHEAD = XS ? 2 : NT <= 2 ? 4 : NT <= 6 ? 2 : 1;   // words of tokens in flight
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) load_x(i);
       cp_async_wait<DEPTH - 1>();
@@ -263,25 +284,39 @@ static bool tc_is_faster(int nt, int64_t N, int64_t K, int64_t K_l, int silu_sha
   return 5.0 + 0.39 * double(tc_steps(N, K_l, silu_shards, shards)) < here;
 }
 
-template <int NT, int R, int DEPTH, bool SILU, bool ZEROS, bool WHOLE>
-static int launch_gemv(GemvArgs a, cudaStream_t st) {
-  auto kern = gemv_kernel<NT, R, DEPTH, SILU, ZEROS, WHOLE>;
-  constexpr size_t smem = kWarps * gemv_warp_smem(NT, R, DEPTH);
+template <int NT, int R, int DEPTH, bool SILU, bool ZEROS, bool WHOLE, bool XS>
+static int start_gemv(const GemvArgs& a, int64_t units, size_t smem, cudaStream_t st) {
+  auto kern = gemv_kernel<NT, R, DEPTH, SILU, ZEROS, WHOLE, XS>;
   if (smem > 48 * 1024) {
-    static const cudaError_t set = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    static const cudaError_t set = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
     if (set != cudaSuccess) return set_error(QW_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(set));
   }
-  const int chunks = (a.pieces + 3) / 4;
-  const int64_t units = (a.tiles + R - 1) / R;
+  const int per_cta = kWarps / a.split;
+  launch_pdl(kern, dim3(unsigned((units + per_cta - 1) / per_cta)), kWarps * 32, smem, st, a);
+  return check_launch("w4 gemv");
+}
+
+template <int NT, int R, int DEPTH, bool SILU, bool ZEROS, bool WHOLE>
+static int launch_gemv(GemvArgs a, cudaStream_t st) {
+  constexpr size_t smem = kWarps * gemv_warp_smem(NT, R, DEPTH);
+  static_assert(smem <= 128 * 1024, "");
   static const int resident = [&] {
+    auto kern = gemv_kernel<NT, R, DEPTH, SILU, ZEROS, WHOLE, false>;
     int n = 0;
+    if (smem > 48 * 1024) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kWarps * 32, smem) == cudaSuccess && n > 0 ? n : 1;
   }();
+  const int chunks = (a.pieces + 3) / 4;
+  const int64_t units = (a.tiles + R - 1) / R;
   a.split = gemv_split(units, chunks, resident);
-  const int per_cta = kWarps / a.split;
-  const dim3 grid(unsigned((units + per_cta - 1) / per_cta));
-  launch_pdl(kern, grid, kWarps * 32, smem, st, a);
-  return check_launch("w4 gemv");
+  if constexpr (WHOLE && NT <= 2) {
+    // us without and with them there: 8 x 151936 x 1024 26.5 / 24.9, 16 x 100000 x 1024 31.2 / 27.4; 8 x 60000 x 4096 (64 KB
+    // of a CTA) 39.0 / 40.4; two tokens or one touch few lines anyway
+    const size_t x_bytes = size_t(chunks) * NT * 2048;
+    if (a.split == 1 && a.M > 2 && x_bytes <= 32 * 1024)
+      return start_gemv<NT, R, DEPTH, SILU, ZEROS, WHOLE, true>(a, units, smem + x_bytes, st);
+  }
+  return start_gemv<NT, R, DEPTH, SILU, ZEROS, WHOLE, false>(a, units, smem, st);
 }
 
 template <int NT, int R, int DEPTH, bool WHOLE>
