@@ -39,7 +39,10 @@ template <bool NARROW> struct Tile {
   static constexpr int EPILOGUE0 = 4 + 4 * SETS, THREADS = 32 * (EPILOGUE0 + 4);
   static constexpr uint32_t X_HALF = TOKENS / 2 * 128, X_BYTES = 2 * X_HALF, C_BYTES = kRows * 128;
   static constexpr uint32_t OFF_X = 0, OFF_C = XS * X_BYTES, OFF_BAR = OFF_C + CS * C_BYTES;
-  static constexpr size_t SMEM = 1024 + OFF_BAR + 512;
+  // More than the stages need: an SM then has no room for a CTA of another kernel that takes TMEM, so that the pairs of
+  // two kernels on two streams cannot each hold the columns that the other's second CTA waits for.
+  static constexpr size_t SMEM = 200 * 1024;
+  static_assert(SMEM >= 1024 + OFF_BAR + 512, "");
   static constexpr uint32_t A = 2 * TOKENS;   // TMEM column of the decoded weights
   static_assert(A + 64 * AS <= 512, "");
   static constexpr int B_X_FULL = 0, B_X_EMPTY = B_X_FULL + XS, B_C_FULL = B_X_EMPTY + XS, B_C_EMPTY = B_C_FULL + CS,
