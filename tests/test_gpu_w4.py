@@ -572,3 +572,16 @@ def test_replayed_graphs_side_by_side(L):
         sync_ok(L)
         for _, _, outs, want, _ in runs:
             assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("epi", [NONE, SILU])
+@pytest.mark.parametrize("M", [3, 8, 11, 16])
+def test_gemm_wide_outputs_of_few_tokens(L, M, epi, zeros):
+    """More row tiles than warps run at once: each warp walks through all of K, the tokens in shared memory."""
+    check_gemm(L, M, 59984, 512, 64, zeros, 1, COL, epi)
+    x = torch.randn(M, 512, generator=gen(M)).bfloat16()
+    x[1] = float("nan")
+    check = run_gemm(L, x.cuda(), *matrix(59984, 512, 64, zeros)[:3], 59984, 64, 1, COL, epi)
+    sync_ok(L)
+    assert torch.isnan(check[1]).all() and torch.isfinite(torch.cat([check[:1], check[2:]])).all()
