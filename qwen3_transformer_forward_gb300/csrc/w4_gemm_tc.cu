@@ -31,17 +31,20 @@ constexpr int kRows = 128;          // weight rows of a CTA (SiluAndMul: 64 gate
 // K advances in steps of 128 columns.  Stages: tokens (a step), codes (two), decoded weights (a step).  TMEM holds two
 // accumulators and the decoded weights.
 template <bool NARROW> struct Tile {
-  static constexpr int TOKENS = NARROW ? 128 : 192, XS = NARROW ? 5 : 4, CS = 4, AS = NARROW ? 4 : 2;
+  static constexpr int TOKENS = NARROW ? 128 : 192, XS = NARROW ? 5 : 4, CS = NARROW ? 8 : 4, AS = NARROW ? 4 : 2;
   static constexpr int SETS = NARROW ? 3 : 2;   // sets of four decoding warps, which take the steps in turn
   // A set's next step lies SETS on and waits for the MMAs of the step AS before that one.  With SETS <= AS it is among
   // those that the set's last step waited for, or that step itself, so a parity is never two phases old.
   static_assert(SETS <= AS, "");
+  // The same for codes: that wait showed that all steps up to SETS + AS before the set's next one had their codes, and
+  // the stage CS before the next one's ends at least CS steps before it (a shard of one step is a stage of its own).
+  static_assert(CS >= SETS + AS, "");
   static constexpr int EPILOGUE0 = 4 + 4 * SETS, THREADS = 32 * (EPILOGUE0 + 4);
   static constexpr uint32_t X_HALF = TOKENS / 2 * 128, X_BYTES = 2 * X_HALF, C_BYTES = kRows * 128;
   static constexpr uint32_t OFF_X = 0, OFF_C = XS * X_BYTES, OFF_BAR = OFF_C + CS * C_BYTES;
   // More than the stages need: an SM then has no room for a CTA of another kernel that takes TMEM, so that the pairs of
   // two kernels on two streams cannot each hold the columns that the other's second CTA waits for.
-  static constexpr size_t SMEM = 200 * 1024;
+  static constexpr size_t SMEM = (NARROW ? 212 : 200) * 1024;
   static_assert(SMEM >= 1024 + OFF_BAR + 512, "");
   static constexpr uint32_t A = 2 * TOKENS;   // TMEM column of the decoded weights
   static_assert(A + 64 * AS <= 512, "");
