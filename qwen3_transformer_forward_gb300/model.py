@@ -298,10 +298,14 @@ class Qwen3Forward:
         # replace (8 x 2048-token prefill: 21.0 ms fused, 19.1 ms unfused)
         self.fused_prefill = False
 
+    def _in_4_bits(self, *names) -> bool:
+        """Some layer holds one of these weights in 4 bits; the others may be bf16."""
+        return any(isinstance(getattr(p, n), W4Weight) for p in self.p.layers for n in names)
+
     @property
     def w4(self) -> bool:
-        """The layers' linear weights are in 4 bits."""
-        return len(self.p.layers) > 0 and isinstance(self.p.layers[0].qkv, W4Weight)
+        """Linear weights of the layers are in 4 bits, all or some."""
+        return self._in_4_bits("qkv", "o", "gate_up", "down")
 
     def _linear(self, A, W, C, N, mode, epilogue, stream=None):
         """One linear layer, over bf16 / f32 or 4-bit weights."""
@@ -334,8 +338,9 @@ class Qwen3Forward:
         """Prefill: QK-norm + RoPE + KV store as the QKV GEMM's epilogue (bf16,
         head_dim 128, two whole heads of one shard per 256-column tile)."""
         m = self.m
-        return (self.fused_qkv and self.kv8 is None and not self.w4 and self.dtype == torch.bfloat16 and m.head_dim == 128
-                and ((m.n_heads + 2 * m.n_kv_heads) // m.tp) % 2 == 0 and m.hidden % 8 == 0)
+        return (self.fused_qkv and self.kv8 is None and self.dtype == torch.bfloat16 and m.head_dim == 128
+                and ((m.n_heads + 2 * m.n_kv_heads) // m.tp) % 2 == 0 and m.hidden % 8 == 0
+                and not self._in_4_bits("qkv"))
 
     def prefill_fusion_ok(self) -> bool:
         """Prefill through the fused epilogues: QK-norm + RoPE + KV store in the QKV
@@ -384,20 +389,21 @@ class Qwen3Forward:
                 L.gemm_add_rmsnorm(act, p.down, res, next_gamma, m.eps, y, tp, stream)
 
     def norm_fusion_ok(self, T: int) -> bool:
-        """Few bf16 tokens: each add+RMSNorm runs as the prologue of the GEMM it feeds."""
-        return self.dtype == torch.bfloat16 and T <= 16 and T <= self.res2.shape[0] and not self.w4
+        """Few bf16 tokens: each add+RMSNorm runs as the prologue of the GEMM it feeds, over bf16 weights in every layer."""
+        return (self.dtype == torch.bfloat16 and T <= 16 and T <= self.res2.shape[0]
+                and not self._in_4_bits("qkv", "gate_up"))
 
     def _res(self, c: int, T: int):
         """Residual after update c of a decode step (two per layer) when norms are fused."""
         return (self.res if c % 2 == 0 else self.res2)[:T]
 
     # -- one decoder layer ([SK] §1) ------------------------------------------
-    def _layer(self, l: int, T: int, ctx, first: bool, decode: bool, stream=None):
+    def _layer(self, l: int, T: int, ctx, first: bool, decode: bool, fused: bool, stream=None):
+        """fused: add+RMSNorm as the prologue of the GEMM that it feeds, in every layer or in none."""
         m, p = self.m, self.p.layers[l]
         tp = m.tp
         h, res, y = self.h[:T], self.res[:T], self.y[:T]
         ph = "decode" if decode else "prefill"
-        fused = decode and self.norm_fusion_ok(T)
         qkv = self.qkv[:T]
         if fused:
             # residual update 2l here, 2l+1 before gate_up; the buffers alternate
@@ -547,10 +553,10 @@ class Qwen3Forward:
             if final_norm:
                 return self.y[:T]   # the last down GEMM applied the final norm
             return self.h[:T], self.res[:T]
+        fused = decode and self.norm_fusion_ok(T)
         for l in range(nl):
-            self._layer(l, T, ctx, l == 0, decode, stream)
-        nl = len(self.p.layers)
-        res = self._res(2 * nl - 1, T) if decode and self.norm_fusion_ok(T) and nl > 0 else self.res[:T]
+            self._layer(l, T, ctx, l == 0, decode, fused, stream)
+        res = self._res(2 * nl - 1, T) if fused and nl > 0 else self.res[:T]
         if not final_norm:
             return self.h[:T], res
         with self._around("final_norm", -1):
