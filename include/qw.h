@@ -613,7 +613,8 @@ size_t qw_sample_workspace_size(int64_t B, int64_t V);
  * qw_w4_quantize: codes, scales and zeros of a matrix w bf16 [N, K], rounding
  * to nearest even throughout.  For each row and group, over its finite weights:
  *   zeros NULL: s = bf16(max|w| / 7);  n = clamp(round(w / s), -8, 7) + 8
- *   zeros:      lo = min(w, 0), hi = max(w, 0), s = bf16((hi - lo) / 15) (hi - lo in fp32),
+ *   zeros:      lo = min(w, 0), hi = max(w, 0), s = bf16((hi - lo) / 15) (hi - lo rounded to
+ *               fp32, but without its limit: no finite weights give an infinite scale),
  *               z = min(round(-lo / s), 15), n = clamp(round(w / s) + z, 0, 15)
  * where s is 0, w / 0 counts as w / 1.  NaN counts as 0, an infinity becomes the
  * largest code of its sign.  A row split W [tp, N, K/tp] (qw_gemm) is quantised
@@ -642,7 +643,8 @@ int qw_w4_embed_vocab(const int64_t* ids, int64_t T, const void* codes, const vo
  *   zeros were complete before the kernel enqueued just before this call
  *   started (weights that were loaded once).  They are then read before that
  *   kernel has ended (programmatic dependent launch); without the flag nothing is.
- * workspace: qw_w4_gemm_workspace_size bytes; may be NULL when that is 0.
+ * workspace: unused, as qw_gemm's (pass NULL, 0); qw_w4_gemm_workspace_size
+ *   returns 0.
  */
 #define QW_W4_WEIGHTS_READY 1
 int qw_w4_gemm(const void* A, const void* codes, const void* scales, const void* zeros, void* C, int64_t M, int64_t N,
@@ -656,7 +658,9 @@ size_t qw_w4_gemm_workspace_size(int64_t M, int64_t N, int64_t K, int tp, int mo
  * zero row), and with next_tokens the argmax over each row of the rounded
  * logits, lowest index on ties.  V any number that tp divides.
  * workspace: qw_w4_lm_head_workspace_size bytes, 16-byte aligned; may be NULL
- * when last_idx and next_tokens both are.  flags: as for qw_w4_gemm.
+ * when last_idx and next_tokens both are.  The picked rows lie in it, behind
+ * the area for counters, which this call leaves alone.  flags: as for
+ * qw_w4_gemm.
  */
 int qw_w4_lm_head(const void* hidden, int64_t T, const int32_t* last_idx, int64_t n_out, const void* codes,
                   const void* scales, const void* zeros, int64_t V, int64_t H, int group, int tp, void* logits,
