@@ -428,9 +428,7 @@ extern "C" int qw_w4_gemm(const void* A, const void* codes, const void* scales, 
   const int rc = w4::check_weights("qw_w4_gemm", codes, scales, N, K_l, group);
   if (rc) return rc;
   if (!A || !C || !al16(A) || !al16(C)) return set_error(QW_ERR_INVALID_ARG, "qw_w4_gemm: null or misaligned A or C");
-  const size_t need = qw_w4_gemm_workspace_size(M, N, K, tp, mode, epilogue);
-  if (need && (!workspace || workspace_bytes < need))
-    return set_error(QW_ERR_WORKSPACE, "qw_w4_gemm: workspace of %zu bytes needed", need);
+  (void)workspace, (void)workspace_bytes;
   return w4::linear(static_cast<const bf16*>(A), codes, scales, zeros, static_cast<bf16*>(C), M, N, K, group, tp, mode,
                     epilogue, flags, static_cast<cudaStream_t>(stream));
 }
