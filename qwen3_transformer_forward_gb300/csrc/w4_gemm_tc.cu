@@ -12,8 +12,9 @@
 // decoding about 400 of the sub-partition's pipes, the MMA warp's waits and issue about 450; so the tensor pipe leads
 // (N of 192 rather than 256 leaves TMEM for the second accumulator: stores overlap the next tile's MMAs).
 // 16384 x 12288 x 2048 with SiluAndMul: 480-496 us, 1.66-1.72 PFLOP/s, the rate that a large library product sustains
-// under the power limit; 4096 x 12288 x 2048: 121 us, 1.70 PFLOP/s.  With few tokens the decoding sets' latency leads:
-// about 365 cycles for 128 rows x 64 columns against 190 of memory (128 x 28672 x 8192 61 us; 65 x 151936 x 1024 36 us).
+// under the power limit; 4096 x 12288 x 2048: 112-121 us, 1.70-1.85 PFLOP/s; 16384 x 2048 x 6144 in two row shards 225 us,
+// 1.83.  With few tokens the decoding sets' latency leads: about 365 cycles for 128 rows x 64 columns, of which the decoding's
+// instructions need 184, against 190 of memory (128 x 28672 x 8192 58 us; 65 x 151936 x 1024 34 us).
 // One CTA for itself with 192 tokens ran at 793 us (tokens' traffic twice), the MMAs issued by one lane in a branch at
 // 1162, arrivals at the other CTA's barriers that release all memory at 887 against 637.
 #include <algorithm>
@@ -500,8 +501,8 @@ static int launch(const CUtensorMap& mx, const CUtensorMap& mc, const TcArgs& a,
 }
 
 // Few tiles: their K in parts, as many as run at once (15 clusters of 8 CTAs, 23 of 6, 36 of 4, 76 pairs).  16 tokens,
-// K 8192, us in 4 / 3 / 2 / 1 parts: 15 tiles 13.4 / 15.2 / 18.5 / 28.6, 16 tiles 23.6 / 14.9 / 18.2 / 28.3,
-// 22 tiles 24.2 / 15.4 / 18.5 / 28.5, 36 tiles 35.6 / 28.8 / 19.0 / 28.9.
+// K 8192, us in 4 / 3 / 2 / 1 parts: 15 tiles 13.5 / 15.5 / 18.5 / 28.6, 16 tiles 23.9 / 15.5 / 18.5 / 28.7,
+// 22 tiles 24.7 / 15.9 / 18.9 / 29.0, 36 tiles 36.6 / 29.7 / 19.7 / 29.6.
 static int parts_of_k(int64_t tiles, int64_t stages) {
   return int(std::min<int64_t>(tiles <= 15 ? 4 : tiles <= 23 ? 3 : tiles <= 36 ? 2 : 1, stages));
 }

@@ -3,10 +3,13 @@
 // out[m, n] = sum_k x[m, k] w[n, k], w decoded from its code, scale and zero point in registers (w4.cuh) and fed to
 // mma.sync m16n8k16 as the A operand: 16 weight rows against 8 tokens, fp32 sums.  A warp's sums of its part of K are
 // added over the warps of a row tile in shared memory, in slice order.
-// Bound: an MMA occupies an SM sub-partition for 16 cycles whatever the number of live tokens, so that a chunk of 16 rows
-// x 128 columns cannot take less than 256 of its cycles; decoding takes 128 of the half-rate bf16 pipe and 112 of the
-// integer pipe beside it.  1 x 28672 x 8192 (117 MB of codes): 30 us, 4.0 TB/s, against 25.4 us for its MMAs and 17.9 for
-// its bytes; 8 x 151936 x 1024: 24.9 us against 16.8 and 12.6; 1 x 4096 x 1024: 2.4 us in a graph, launch and latency.
+// Bound: the operands' way through L1, then the chain of a chunk.  A chunk of 16 rows x 128 columns is 8 MMAs, and one
+// occupies an SM sub-partition for 8 cycles (measured in a loop of them alone), 64 in all; decoding takes 128 of the
+// half-rate bf16 pipe and 112 of the integer pipe beside it.  1 x 28672 x 8192 (117 MB of codes): 31.5 us, 3.8 TB/s, against
+// 17.9 for its bytes and 6.2 for its MMAs; L1 is at 85% of its peak there (codes cross it on their way into shared memory
+// and out of it, scales in loads of two bytes a row, tokens again for each row tile), the tensor pipe at 22%.  8 x 151936 x
+// 1024, its tokens in shared memory: 24.9 us against 12.6 and 4.1, no unit above 53% (issue slots).  1 x 4096 x 1024: 2.4 us
+// in a graph, launch and latency.
 #include "w4.cuh"
 
 namespace qw {
@@ -276,8 +279,8 @@ static int gemv_split(int64_t units, int chunks, int resident) {
 // 9 to 64 tokens: whether the tcgen05 kernel is expected to be done first.  Both sides from measurements: a step of
 // 256 rows x 128 columns takes a pair of SMs 0.39 us, the launch and its ends about 5; here 2.5 us and 0.21, 0.39, 0.46,
 // 0.46, 0.6 and 0.78 us for each 2^20 weights with 2, 3, 4, 5, 6 and 8 groups of 8 tokens.  us there and here:
-// 8192 x 8192, 16 tokens 19.0 / 15.7, 24 19.3 / 20.8, 64 20.4 / 50.2; 4096 x 4096, 24 11.3 / 8.7, 64 12.2 / 15.6;
-// 4096 x 1024, 64 8.4 / 7.2; 151936 x 1024, 16 31.2 / 36.5, 64 32.7 / 145.
+// 8192 x 8192, 16 tokens 19.5 / 17.3, 24 19.9 / 26.5, 64 21.0 / 49.2; 4096 x 4096, 24 11.5 / 9.1, 64 12.4 / 16.8;
+// 4096 x 1024, 64 8.3 / 7.5; 151936 x 1024, 16 32.3 / 34.5, 64 33.3 / 146.
 static bool tc_is_faster(int nt, int64_t N, int64_t K, int64_t K_l, int silu_shards, int shards) {
   static const double per_mega[9] = {0, 0, 0.21, 0.39, 0.46, 0.46, 0.6, 0.78, 0.78};
   const double here = 2.5 + per_mega[nt] * double(N) * double(K) / (1 << 20);

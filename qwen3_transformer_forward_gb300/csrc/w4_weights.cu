@@ -15,8 +15,9 @@ namespace w4 {
 // rounds it to a multiple of 2^-11: ties become exact again and nothing else becomes one.  Adding 1.5 * 2^23 less that
 // then rounds to an integer, ties to even, which stands in the low bits.  In the symmetric form |w / s| < 7.1 needs no
 // clamp, in the asymmetric form only the upper end does (both roundings may go up).
-// Bound by memory, with the small stores of scales and zero points: 151936 x 1024, group 32, 399 MB in 72 us symmetric
-// (5.5 TB/s) and 404 MB in 93 us asymmetric (4.3 TB/s).  With a division for each weight: 170 us.
+// Bound by its instructions, 15 a weight symmetric and 18 asymmetric: issue slots are used to 78-79% in both forms, memory
+// to 65 and 54%.  151936 x 1024, group 32: 399 MB in 72 us symmetric (5.5 TB/s), 404 MB in 91 us asymmetric (4.4 TB/s).
+// With a division for each weight: 170 us.
 // ---------------------------------------------------------------------------
 constexpr int kQuant = 4;
 constexpr float kSnap = 6144.0f, kInt = 12582912.0f;   // 1.5 * 2^12, 1.5 * 2^23
